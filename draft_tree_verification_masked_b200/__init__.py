@@ -16,6 +16,9 @@ Entry points (same names as the C ABI in ``include/etree.h``)::
                              path, out_tokens, zbuf, workspace)
     etree_kv_compact(batch, accept_len, path, k_tree, v_tree, k_cache, v_cache, n_layers,
                      tree_layer_stride, cache_layer_stride, kv_len_out, workspace)
+    etree_page_plan(cu_new, kv_len, page_size, num_pages, pages_held, free_ring, ring_state,
+                    block_table, pages_held_out, ring_state_out, slot_cap, slot_map, workspace)
+    etree_kv_store(slot_map, k, v, k_pool, v_pool, workspace)
     etree_device_status(workspace, stream=None) -> (status, detail)
 """
 from __future__ import annotations
@@ -32,7 +35,7 @@ __all__ = [
     "etree_kv_compact",
     "etree_verify_attn_paged", "etree_kv_compact_paged", "etree_verify_cost", "etree_plan_tree",
     "cost_table", "load_cost_table", "etree_lowrank_workspace_size",
-    "etree_lowrank_candidates", "etree_device_status", "etree_selftest_timeout", "etree_strerror",
+    "etree_lowrank_candidates", "etree_page_plan", "etree_kv_store", "etree_device_status", "etree_selftest_timeout", "etree_strerror",
     "etree_version", "etree_attn_plan", "STATUS",
 ]
 
@@ -43,7 +46,8 @@ STATUS = {0: "ETREE_OK", -1: "ETREE_EINVAL", -2: "ETREE_EUNSUPPORTED", -3: "ETRE
           -4: "ETREE_EDEVICE", -5: "ETREE_ETIMEOUT", -6: "ETREE_ENOSPACE"}
 DETAIL = {0: "none", 1: "bad parent", 2: "bad node count", 3: "bad kv_len", 4: "capacity",
           5: "not a chain", 6: "bad path", 7: "attention wait", 8: "gemm wait", 9: "bad token",
-          10: "logit rows", 11: "bad page", 12: "self-test wait", 13: "walk wait"}
+          10: "logit rows", 11: "bad page", 12: "self-test wait", 13: "walk wait", 14: "free ring",
+          15: "bad slot"}
 
 EXPORTS = ["etree_workspace_size", "etree_workspace_init", "etree_verify_attn",
            "etree_verify_attn_paged", "etree_kv_compact_paged", "etree_verify_cost",
@@ -51,7 +55,7 @@ EXPORTS = ["etree_workspace_size", "etree_workspace_init", "etree_verify_attn",
            "etree_lmhead_accept", "etree_lmhead_accept_tree", "etree_lmhead_accept_timed",
            "etree_kv_compact", "etree_device_status", "etree_strerror",
            "etree_version", "etree_last_error", "etree_attn_plan", "etree_verify_attn_noalloc",
-           "etree_selftest_timeout"]
+           "etree_selftest_timeout", "etree_page_plan", "etree_kv_store"]
 
 
 class EtreeError(RuntimeError):
@@ -125,6 +129,12 @@ def lib():
                                          i64, C.c_int, i64, i64, C.c_int, C.c_int, vp, vp,
                                          C.c_size_t, vp]
     L.etree_kv_compact_paged.restype = C.c_int
+    L.etree_page_plan.argtypes = [i32, i32, vp, vp, i32, i32, i64, vp, vp, vp, vp, vp, vp, vp, vp,
+                                  vp, C.c_size_t, vp]
+    L.etree_page_plan.restype = C.c_int
+    L.etree_kv_store.argtypes = [vp, i32, vp, i64, vp, i64, vp, vp, i64, C.c_int, C.c_int, vp,
+                                 C.c_size_t, vp]
+    L.etree_kv_store.restype = C.c_int
     L.etree_device_status.argtypes = [vp, vp, C.POINTER(i32)]
     L.etree_device_status.restype = C.c_int
     L.etree_selftest_timeout.argtypes = [vp, C.c_size_t, vp]
@@ -419,6 +429,81 @@ def etree_kv_compact(batch: Batch, accept_len, path, k_tree, v_tree, k_cache, v_
         int(tree_layer_stride), int(cache_layer_stride), hkv, d,
         _ptr(kv_len_out, torch.int32, "kv_len_out"), _ptr(workspace, torch.uint8, "workspace"),
         workspace.numel(), _stream(stream))
+    return _check(st) if check else st
+
+
+def _here(*tensors):
+    """Calls run on the current device's stream: tensors of another device are refused."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.is_cuda and t.device.index != dev:
+            raise ValueError(f"a tensor lives on {t.device}, the current device is cuda:{dev}")
+
+
+def _numel(t, n: int, name: str):
+    if t is not None and t.numel() != n:
+        raise ValueError(f"{name} must hold {n} entries, got {tuple(t.shape)}")
+
+
+def etree_page_plan(cu_new, kv_len, page_size: int, num_pages: int, pages_held, free_ring,
+                    ring_state, block_table, pages_held_out, ring_state_out, slot_cap, slot_map,
+                    workspace, stream=None, check: bool = True) -> int:
+    """Block tables and slot maps from request lengths.  cu_new int32 [B + 1], kv_len and
+    pages_held int32 [B], free_ring int32 [num_pages], ring_state int64 [2], block_table int32
+    [B, max_pages] (updated in place); slot_cap int32 [B] and slot_map int64 may be None."""
+    i32, i64 = torch.int32, torch.int64
+    B = kv_len.numel()
+    for t, n, name in ((cu_new, B + 1, "cu_new"), (pages_held, B, "pages_held"),
+                       (free_ring, int(num_pages), "free_ring"), (ring_state, 2, "ring_state"),
+                       (pages_held_out, B, "pages_held_out"),
+                       (ring_state_out, 2, "ring_state_out"), (slot_cap, B, "slot_cap"),
+                       (block_table, B * block_table.shape[-1], "block_table")):
+        _numel(t, n, name)
+    args = (
+        B, 0 if slot_map is None else slot_map.numel(), _ptr(cu_new, i32, "cu_new"),
+        _ptr(kv_len, i32, "kv_len"), int(page_size), block_table.shape[-1], int(num_pages),
+        _ptr(pages_held, i32, "pages_held"), _ptr(free_ring, i32, "free_ring"),
+        _ptr(ring_state, i64, "ring_state"), _ptr(block_table, i32, "block_table"),
+        _ptr(pages_held_out, i32, "pages_held_out"), _ptr(ring_state_out, i64, "ring_state_out"),
+        _ptr(slot_cap, i32, "slot_cap"), _ptr(slot_map, i64, "slot_map"),
+        _ptr(workspace, torch.uint8, "workspace"), workspace.numel())
+    _here(cu_new, kv_len, pages_held, free_ring, ring_state, block_table, pages_held_out,
+          ring_state_out, slot_cap, slot_map, workspace)
+    st = lib().etree_page_plan(*args, _stream(stream))
+    return _check(st) if check else st
+
+
+def _rows(t, name: str):
+    """Pointer and row stride of a [rows, heads, dims] bf16 tensor whose rows are dense inside."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on a CUDA device")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    n, h, d = t.shape
+    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}: a row's heads must be contiguous")
+    return t.data_ptr(), (t.stride(0) if n > 1 else h * d)
+
+
+def etree_kv_store(slot_map, k, v, k_pool, v_pool, workspace, stream=None,
+                   check: bool = True) -> int:
+    """slot_map int64 [n]; k, v bf16 [n, hkv, 128], rows any stride apart (views of a fused
+    projection, say); pools bf16 [slots, hkv, 128]."""
+    bf = torch.bfloat16
+    n, hkv, d = k.shape
+    if tuple(v.shape) != (n, hkv, d) or tuple(k_pool.shape[1:]) != (hkv, d) or \
+            k_pool.shape != v_pool.shape:
+        raise ValueError("k, v and the pools must have the same heads")
+    _numel(slot_map, n, "slot_map")
+    kp, ks = _rows(k, "k")
+    vp, vs = _rows(v, "v")
+    args = (_ptr(slot_map, torch.int64, "slot_map"), n, kp, ks, vp, vs,
+            _ptr(k_pool, bf, "k_pool"), _ptr(v_pool, bf, "v_pool"), k_pool.shape[0], hkv, d,
+            _ptr(workspace, torch.uint8, "workspace"), workspace.numel())
+    _here(slot_map, k, v, k_pool, v_pool, workspace)
+    st = lib().etree_kv_store(*args, _stream(stream))
     return _check(st) if check else st
 
 

@@ -968,6 +968,119 @@ etree_status etree_kv_compact_paged(const etree_batch* b, const int32_t* block_t
                          num_pages * page_size, workspace, workspace_bytes, stream);
 }
 
+// Host-visible overlap of two buffers (device addresses, compared as numbers).
+static bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return a && b && x < y + nb && y < x + na;
+}
+
+static etree_status check_header_ws(const void* ws, size_t bytes) {
+  if (!ws || bytes < sizeof(WsHeader) || ((uintptr_t)ws & 255))
+    return fail(ETREE_EINVAL, "workspace is NULL, smaller than its header or misaligned");
+  return ETREE_OK;
+}
+
+etree_status etree_page_plan(int32_t B, int32_t n_tokens, const int32_t* cu_new,
+                             const int32_t* kv_len, int32_t page_size, int32_t max_pages,
+                             int64_t num_pages, const int32_t* pages_held, int32_t* free_ring,
+                             const int64_t* ring_state, int32_t* block_table,
+                             int32_t* pages_held_out, int64_t* ring_state_out, int32_t* slot_cap,
+                             int64_t* slot_map, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  if (B < 1 || B > ETREE_MAX_REQUESTS)
+    return fail(ETREE_EINVAL, "B=%d outside [1, %d]", B, ETREE_MAX_REQUESTS);
+  if (n_tokens < 0) return fail(ETREE_EINVAL, "n_tokens=%d", n_tokens);
+  if (!cu_new || !kv_len || !pages_held || !free_ring || !ring_state || !pages_held_out ||
+      !ring_state_out)
+    return fail(ETREE_EINVAL, "a pointer is NULL");
+  const PagedArgs pg{block_table, max_pages, page_size};
+  etree_status st = check_paged(&pg, num_pages);
+  if (st) return st;
+  if ((int64_t)max_pages * page_size > INT32_MAX)
+    return fail(ETREE_EINVAL, "max_pages=%d: need max_pages * page_size < 2^31", max_pages);
+  for (const void* q : {(const void*)cu_new, (const void*)kv_len, (const void*)pages_held,
+                        (const void*)free_ring, (const void*)pages_held_out,
+                        (const void*)slot_cap})
+    if ((uintptr_t)q & 3) return fail(ETREE_EINVAL, "an int32 array is misaligned");
+  for (const void* q : {(const void*)ring_state, (const void*)ring_state_out,
+                        (const void*)slot_map})
+    if ((uintptr_t)q & 7) return fail(ETREE_EINVAL, "an int64 array is misaligned");
+  if ((st = check_header_ws(workspace, workspace_bytes))) return st;
+  // every CTA of the launch reads all inputs: no output may share memory with one, or with another
+  const size_t nb = (size_t)B * 4;
+  const struct { const void* p; size_t n; } in[] = {
+      {cu_new, nb + 4}, {kv_len, nb}, {pages_held, nb}, {ring_state, 16},
+  }, out[] = {
+      {free_ring, (size_t)num_pages * 4}, {block_table, (size_t)B * max_pages * 4},
+      {pages_held_out, nb}, {ring_state_out, 16}, {slot_cap, nb}, {slot_map, (size_t)n_tokens * 8},
+  };
+  for (int i = 0; i < 6; ++i) {
+    for (const auto& x : in)
+      if (overlaps(x.p, x.n, out[i].p, out[i].n))
+        return fail(ETREE_EINVAL, "an output aliases an input");
+    for (int j = 0; j < i; ++j)
+      if (overlaps(out[j].p, out[j].n, out[i].p, out[i].n))
+        return fail(ETREE_EINVAL, "two outputs alias");
+  }
+  PlanParams p{};
+  p.cu_new = cu_new;
+  p.kv_len = kv_len;
+  p.held = pages_held;
+  p.ring = free_ring;
+  p.ring_state = ring_state;
+  p.block_table = block_table;
+  p.held_out = pages_held_out;
+  p.ring_state_out = ring_state_out;
+  p.slot_cap = slot_cap;
+  p.slot_map = slot_map;
+  p.ws = at<WsHeader>(workspace, 0);
+  p.B = B;
+  p.n_tokens = n_tokens;
+  p.max_pages = max_pages;
+  p.page_shift = log2i(page_size);
+  p.num_pages = num_pages;
+  const cudaError_t e = launch_page_plan(p, sm_count(), static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ETREE_OK : cuda_fail(e, "etree_page_plan launch");
+}
+
+etree_status etree_kv_store(const int64_t* slot_map, int32_t n_tokens, const uint16_t* k,
+                            int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                            uint16_t* k_pool, uint16_t* v_pool, int64_t num_slots, int hkv,
+                            int head_dim, void* workspace, size_t workspace_bytes, void* stream) {
+  if (head_dim != ETREE_HEAD_DIM)
+    return fail(ETREE_EUNSUPPORTED, "head_dim=%d (only 128 is built)", head_dim);
+  if (hkv < 1 || hkv > 65535) return fail(ETREE_EINVAL, "hkv=%d", hkv);
+  if (n_tokens < 0) return fail(ETREE_EINVAL, "n_tokens=%d", n_tokens);
+  const int64_t row = (int64_t)hkv * head_dim;
+  if (k_stride < row || v_stride < row || k_stride % 8 || v_stride % 8)
+    return fail(ETREE_EINVAL, "k_stride=%lld, v_stride=%lld: need multiples of 8 of at least %lld",
+                (long long)k_stride, (long long)v_stride, (long long)row);
+  if (num_slots < 1 || num_slots > INT32_MAX)
+    return fail(ETREE_EINVAL, "num_slots=%lld outside [1, 2^31)", (long long)num_slots);
+  if (!k_pool || !v_pool || (n_tokens > 0 && (!slot_map || !k || !v)))
+    return fail(ETREE_EINVAL, "a pointer is NULL");
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_pool) || !aligned16(v_pool) ||
+      ((uintptr_t)slot_map & 7))
+    return fail(ETREE_EINVAL, "K/V tensors must be 16-byte aligned, slot_map 8-byte aligned");
+  etree_status st = check_header_ws(workspace, workspace_bytes);
+  if (st) return st;
+  if (n_tokens == 0) return ETREE_OK;
+  StoreParams p{};
+  p.slot_map = slot_map;
+  p.k = reinterpret_cast<const uint4*>(k);
+  p.v = reinterpret_cast<const uint4*>(v);
+  p.k_pool = reinterpret_cast<uint4*>(k_pool);
+  p.v_pool = reinterpret_cast<uint4*>(v_pool);
+  p.ws = at<WsHeader>(workspace, 0);
+  p.n_tokens = n_tokens;
+  p.hkv = hkv;
+  p.k_stride16 = k_stride / 8;
+  p.v_stride16 = v_stride / 8;
+  p.num_slots = num_slots;
+  const cudaError_t e = launch_kv_store(p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ETREE_OK : cuda_fail(e, "etree_kv_store launch");
+}
+
 // Tree attention without a caller workspace: the split partials and the status words live in
 // the library's static scratch array (see etree.h for the contract).
 etree_status etree_verify_attn_noalloc(const etree_batch* b, const uint16_t* q,

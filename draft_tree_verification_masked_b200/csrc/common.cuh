@@ -37,6 +37,8 @@ enum Detail : int32_t {
   DET_BAD_PAGE = 11,        // a block-table entry outside [0, num_pages) for a used position
   DET_SELFTEST = 12,        // etree_selftest_timeout: the deliberately unfinished wait gave up
   DET_WAIT_WALK = 13,       // the tree walk gave up waiting for another CTA's residual slice
+  DET_FREE_RING = 14,       // the free ring's head and tail do not fit its pages (etree_page_plan)
+  DET_BAD_SLOT = 15,        // a slot below -1 or past the pool (etree_kv_store)
 };
 
 __device__ __forceinline__ void report(WsHeader* ws, int32_t code, int32_t detail) {

@@ -160,4 +160,33 @@ struct CompactParams {
 };
 cudaError_t launch_compact(const CompactParams& p, int ctas, cudaStream_t s);
 
+struct PlanParams {
+  const int32_t* cu_new;
+  const int32_t* kv_len;
+  const int32_t* held;
+  int32_t* ring;                    // free page ids, a ring of num_pages entries
+  const int64_t* ring_state;        // [2] head and tail: ids [head, tail) modulo num_pages are free
+  int32_t* block_table;
+  int32_t* held_out;
+  int64_t* ring_state_out;
+  int32_t* slot_cap;                // may be null
+  int64_t* slot_map;                // may be null
+  WsHeader* ws;
+  int B, n_tokens, max_pages, page_shift;
+  int64_t num_pages;
+};
+cudaError_t launch_page_plan(const PlanParams& p, int sms, cudaStream_t s);
+
+struct StoreParams {
+  const int64_t* slot_map;
+  const uint4* k;
+  const uint4* v;
+  uint4* k_pool;
+  uint4* v_pool;
+  WsHeader* ws;
+  int n_tokens, hkv;
+  int64_t k_stride16, v_stride16, num_slots;
+};
+cudaError_t launch_kv_store(const StoreParams& p, cudaStream_t s);
+
 }  // namespace etree

@@ -313,6 +313,65 @@ etree_status etree_kv_compact_paged(const etree_batch *batch, const int32_t *blo
                                     size_t workspace_bytes, void *stream);
 
 /*
+ * Page plan: block tables and slot maps from request lengths, on the device.  Every sequence grows
+ * by its own accepted length each step ("Eagle-4 Released ...", section "Current Limitation"), so
+ * a paged engine learns only on the device which pages a step needs; this call gives each request
+ * its pages without a read by the host, and its outputs feed etree_verify_attn_paged,
+ * etree_kv_compact_paged (block_table, slot_cap) and etree_kv_store (slot_map).
+ * Request r holds kv_len[r] cached tokens and appends new_r = cu_new[r+1] - cu_new[r] (the nodes of
+ * its tree, or a prompt's tokens; 0 is allowed).  With P = page_size it needs
+ * need_r = ceil((kv_len[r] + new_r) / P) pages and holds pages_held[r]:
+ *  - need_r > pages_held[r]: it takes the difference from the head of the free ring, into
+ *    block_table[r][pages_held[r] .. need_r);
+ *  - need_r < pages_held[r]: block_table[r][need_r .. pages_held[r]) go to the tail of the ring, in
+ *    that order (a finished request passes kv_len 0 and no new tokens, and gives back all).  They
+ *    are free from the next call on.
+ * Requests take pages in their order.  A request whose pages, with those of the growing requests
+ * before it, pass the ids that were free at the start is not served, nor is any later request
+ * that grows: they keep what they hold, their slots are -1, and ETREE_ENOSPACE (detail 4) is
+ * recorded.  Results do not depend on timing.
+ *   cu_new         [B+1] int32, cu_new[0] = 0;  kv_len [B] int32
+ *   pages_held     [B] int32, pages in use of each row of the block table
+ *   free_ring      [num_pages] int32, ring_state [2] int64 = (head, tail), 0 <= head <= tail: the
+ *                  ids free_ring[i % num_pages], head <= i < tail, are free
+ *   block_table    [B][max_pages] int32, updated in place; other entries are left as they were
+ *   pages_held_out [B], ring_state_out [2]: the new state (buffers of their own, as kv_len_out is)
+ *   slot_cap       [B] int32 pages_held_out * P, or NULL
+ *   slot_map       [n_tokens] int64 pool slot of each new token, -1 behind cu_new[B] and where a
+ *                  request is not served; cu_new[B] <= n_tokens.  Or NULL (n_tokens is then unused)
+ * page_size and num_pages as for etree_verify_attn_paged, max_pages * page_size < 2^31.  No output
+ * may overlap an input or another output (ETREE_EINVAL).  The workspace needs only its 256-byte
+ * status header.  A request with new_r < 0 or cu_new out of range (ETREE_EDEVICE, detail 2), with
+ * a negative length, pages_held outside [0, max_pages] or more tokens than max_pages hold
+ * (detail 3) is left as it is, its slots -1.  A ring state that does not fit the ring, before or
+ * with the pages given back, records detail 14: nothing is then given back (nor taken, when the
+ * state itself is wrong).  A page id outside [0, num_pages) under a new token records detail 11 and
+ * its slot is -1.  Two calls that share a ring or a block table must be ordered.
+ */
+etree_status etree_page_plan(int32_t B, int32_t n_tokens, const int32_t *cu_new,
+                             const int32_t *kv_len, int32_t page_size, int32_t max_pages,
+                             int64_t num_pages, const int32_t *pages_held, int32_t *free_ring,
+                             const int64_t *ring_state, int32_t *block_table,
+                             int32_t *pages_held_out, int64_t *ring_state_out, int32_t *slot_cap,
+                             int64_t *slot_map, void *workspace, size_t workspace_bytes,
+                             void *stream);
+
+/*
+ * K/V store: the rows of new tokens (a prompt's, say) into the pool slots of a slot map,
+ *   pool[slot_map[i]] <- (k, v)[i],  0 <= i < n_tokens.
+ * Row i of k is [hkv][head_dim] bf16 at k + i * k_stride elements, so that rows are read in place
+ * out of a fused projection; likewise v.  Strides are multiples of 8 of at least hkv * head_dim.
+ * Pools as for etree_verify_attn_paged with num_slots = num_pages * page_size rows.  A slot of -1
+ * is skipped; one below -1 or past the pool is skipped and records ETREE_EDEVICE (detail 15).  Two
+ * tokens with one slot leave either's row there.  The rows must not overlap the pools.  The
+ * workspace needs only its 256-byte status header.
+ */
+etree_status etree_kv_store(const int64_t *slot_map, int32_t n_tokens, const uint16_t *k,
+                            int64_t k_stride, const uint16_t *v, int64_t v_stride,
+                            uint16_t *k_pool, uint16_t *v_pool, int64_t num_slots, int hkv,
+                            int head_dim, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * Low-rank candidate head: screen the vocabulary with a factorised projection, then score only
  * the survivors exactly.  EAGLE-4's draft uses such a head in place of its full vocabulary
  * projection ("EAGLE-4 是什麼？...", aiposthub.com, section "EAGLE-4 是什麼？先看推測解碼為什麼能變快",
@@ -402,6 +461,8 @@ etree_status etree_plan_tree(const etree_cost_table *table, int32_t B, int32_t L
  *   11  bad page: a block-table entry outside [0, num_pages) for a used position
  *   12  self-test wait: etree_selftest_timeout's deliberately unfinished wait gave up
  *   13  walk wait: the tree walk gave up waiting for another CTA's part of a residual sum
+ *   14  free ring: a free ring whose head and tail do not fit its pages (etree_page_plan)
+ *   15  bad slot: a slot below -1 or past the pool (etree_kv_store)
  */
 etree_status etree_device_status(void *workspace, void *stream, int32_t *detail);
 
