@@ -19,6 +19,9 @@ Entry points (same names as the C ABI in ``include/etree.h``)::
     etree_page_plan(cu_new, kv_len, page_size, num_pages, pages_held, free_ring, ring_state,
                     block_table, pages_held_out, ring_state_out, slot_cap, slot_map, workspace)
     etree_kv_store(slot_map, k, v, k_pool, v_pool, workspace)
+    etree_verify_attn_diff(batch, q, k_tree, v_tree, k_cache, v_cache, scale, lam, norm_w,
+                           norm_eps, out_scale, out, lse, workspace)
+    etree_verify_attn_diff_paged(batch, block_table, page_size, q, ...)
     etree_device_status(workspace, stream=None) -> (status, detail)
 """
 from __future__ import annotations
@@ -35,7 +38,9 @@ __all__ = [
     "etree_kv_compact",
     "etree_verify_attn_paged", "etree_kv_compact_paged", "etree_verify_cost", "etree_plan_tree",
     "cost_table", "load_cost_table", "etree_lowrank_workspace_size",
-    "etree_lowrank_candidates", "etree_page_plan", "etree_kv_store", "etree_device_status", "etree_selftest_timeout", "etree_strerror",
+    "etree_lowrank_candidates", "etree_page_plan", "etree_kv_store",
+    "etree_attn_diff_workspace_size", "etree_verify_attn_diff", "etree_verify_attn_diff_paged",
+    "etree_device_status", "etree_selftest_timeout", "etree_strerror",
     "etree_version", "etree_attn_plan", "STATUS",
 ]
 
@@ -55,7 +60,9 @@ EXPORTS = ["etree_workspace_size", "etree_workspace_init", "etree_verify_attn",
            "etree_lmhead_accept", "etree_lmhead_accept_tree", "etree_lmhead_accept_timed",
            "etree_kv_compact", "etree_device_status", "etree_strerror",
            "etree_version", "etree_last_error", "etree_attn_plan", "etree_verify_attn_noalloc",
-           "etree_selftest_timeout", "etree_page_plan", "etree_kv_store"]
+           "etree_selftest_timeout", "etree_page_plan", "etree_kv_store",
+           "etree_attn_diff_workspace_size", "etree_verify_attn_diff",
+           "etree_verify_attn_diff_paged"]
 
 
 class EtreeError(RuntimeError):
@@ -135,6 +142,14 @@ def lib():
     L.etree_kv_store.argtypes = [vp, i32, vp, i64, vp, i64, vp, vp, i64, C.c_int, C.c_int, vp,
                                  C.c_size_t, vp]
     L.etree_kv_store.restype = C.c_int
+    L.etree_attn_diff_workspace_size.argtypes = [bp, C.c_int, C.c_int]
+    L.etree_attn_diff_workspace_size.restype = C.c_size_t
+    tail = [i64, C.c_int, C.c_int, C.c_int, f32, vp, vp, f32, f32, vp, vp, vp, C.c_size_t, vp]
+    rows = [vp, i64, vp, i64, vp, i64, vp, vp]
+    L.etree_verify_attn_diff.argtypes = [bp, *rows, *tail]
+    L.etree_verify_attn_diff.restype = C.c_int
+    L.etree_verify_attn_diff_paged.argtypes = [bp, vp, i32, i32, *rows, *tail]
+    L.etree_verify_attn_diff_paged.restype = C.c_int
     L.etree_device_status.argtypes = [vp, vp, C.POINTER(i32)]
     L.etree_device_status.restype = C.c_int
     L.etree_selftest_timeout.argtypes = [vp, C.c_size_t, vp]
@@ -504,6 +519,62 @@ def etree_kv_store(slot_map, k, v, k_pool, v_pool, workspace, stream=None,
             _ptr(workspace, torch.uint8, "workspace"), workspace.numel())
     _here(slot_map, k, v, k_pool, v_pool, workspace)
     st = lib().etree_kv_store(*args, _stream(stream))
+    return _check(st) if check else st
+
+
+def etree_attn_diff_workspace_size(batch: Batch, hq: int, hkv: int) -> int:
+    return int(lib().etree_attn_diff_workspace_size(C.byref(batch), int(hq), int(hkv)))
+
+
+def _diff_args(batch, q, k_tree, v_tree, k_cache, v_cache, slots, scale, lam, norm_w, norm_eps,
+               out_scale, out, lse, workspace):
+    """The arguments that the contiguous and the paged call share, checked."""
+    bf, f32 = torch.bfloat16, torch.float32
+    n, hq, d = q.shape
+    hkv = k_tree.shape[1]
+    if n != batch.n_total or tuple(k_tree.shape) != (n, hkv, d) or v_tree.shape != k_tree.shape:
+        raise ValueError(f"q, k_tree and v_tree must hold {batch.n_total} nodes of {d} dims")
+    if tuple(k_cache.shape[1:]) != (hkv, d) or k_cache.shape != v_cache.shape:
+        raise ValueError("the caches must have k_tree's heads")
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    _numel(lam, hq, "lam")
+    _numel(norm_w, d, "norm_w")
+    _numel(lse, n * hq * 2, "lse")
+    (qp, qs), (kp, ks), (vp, vs) = _rows(q, "q"), _rows(k_tree, "k_tree"), _rows(v_tree, "v_tree")
+    _here(q, k_tree, v_tree, k_cache, v_cache, lam, norm_w, out, lse, workspace)
+    return (qp, qs, kp, ks, vp, vs, _ptr(k_cache, bf, "k_cache"), _ptr(v_cache, bf, "v_cache"),
+            slots, hq, hkv, d, float(scale), _ptr(lam, f32, "lam"), _ptr(norm_w, bf, "norm_w"),
+            float(norm_eps), float(out_scale), _ptr(out, bf, "out"), _ptr(lse, f32, "lse"),
+            _ptr(workspace, torch.uint8, "workspace"), workspace.numel())
+
+
+def etree_verify_attn_diff(batch: Batch, q, k_tree, v_tree, k_cache, v_cache, scale: float, lam,
+                           norm_w, norm_eps: float, out_scale: float, out, lse, workspace,
+                           stream=None, check: bool = True) -> int:
+    """Differential tree attention.  q, k_tree, v_tree bf16 [n, heads, 128], rows any stride
+    apart; lam fp32 [hq]; norm_w bf16 [128] or None; lse fp32 [n, hq, 2] or None."""
+    st = lib().etree_verify_attn_diff(
+        C.byref(batch), *_diff_args(batch, q, k_tree, v_tree, k_cache, v_cache, k_cache.shape[0],
+                                    scale, lam, norm_w, norm_eps, out_scale, out, lse, workspace),
+        _stream(stream))
+    return _check(st) if check else st
+
+
+def etree_verify_attn_diff_paged(batch: Batch, block_table, page_size: int, q, k_tree, v_tree,
+                                 k_pool, v_pool, scale: float, lam, norm_w, norm_eps: float,
+                                 out_scale: float, out, lse, workspace, stream=None,
+                                 check: bool = True) -> int:
+    """The same over pools [num_pages * page_size, hkv, 128]; block_table int32 [B, max_pages]."""
+    if block_table.numel() != batch.B * block_table.shape[-1]:
+        raise ValueError(f"block_table must have {batch.B} rows")
+    _here(block_table)
+    st = lib().etree_verify_attn_diff_paged(
+        C.byref(batch), _ptr(block_table, torch.int32, "block_table"), block_table.shape[-1],
+        int(page_size), *_diff_args(batch, q, k_tree, v_tree, k_pool, v_pool,
+                                    k_pool.shape[0] // max(1, int(page_size)), scale, lam, norm_w,
+                                    norm_eps, out_scale, out, lse, workspace),
+        _stream(stream))
     return _check(st) if check else st
 
 

@@ -145,18 +145,19 @@ static EncodeTiledFn encode_fn() {
 
 struct MapKey {
   uintptr_t ptr;
-  uint64_t d0, d1, d2, rs;
+  uint64_t d0, d1, d2, rs, ps;
   uint32_t b0, b1, b2, rank;
   int dev;
   bool operator==(const MapKey& o) const {
     return ptr == o.ptr && d0 == o.d0 && d1 == o.d1 && d2 == o.d2 && rs == o.rs && b0 == o.b0 &&
-           b1 == o.b1 && b2 == o.b2 && rank == o.rank && dev == o.dev;
+           b1 == o.b1 && b2 == o.b2 && rank == o.rank && dev == o.dev && ps == o.ps;
   }
 };
 struct MapKeyHash {
   size_t operator()(const MapKey& k) const {
     size_t h = std::hash<uintptr_t>()(k.ptr);
-    h ^= std::hash<uint64_t>()(k.d0 * 1315423911u + k.d1 * 2654435761u + k.d2 + k.rs * 40503u) +
+    h ^= std::hash<uint64_t>()(k.d0 * 1315423911u + k.d1 * 2654435761u + k.d2 + k.rs * 40503u +
+                               k.ps * 69069u) +
          0x9e3779b9 + (h << 6) + (h >> 2);
     h ^= (size_t)k.b0 * 31 + k.b1 * 17 + k.b2 * 7 + k.rank + (size_t)k.dev * 101;
     return h;
@@ -169,13 +170,14 @@ static std::unordered_map<MapKey, CUtensorMap, MapKeyHash> g_maps;
 // bf16 tensor map with 128-byte swizzle.  rank 2: dims {d0, d1}, row stride d0*2 bytes;
 // rank 3: dims {d0, d1, d2}, strides {d0*2, d0*d1*2}.  Cached per (pointer, shape, box, device).
 // A bf16 tensor map with 128-byte swizzle, dims {d0 (contiguous), d1, d2}, box {b0, b1, b2}.  Rows
-// (dimension 1) are row_bytes apart, or d0 * 2 bytes when row_bytes is 0.  Cached per key.
+// (dimension 1) are row_bytes apart, or d0 * 2 bytes when row_bytes is 0; planes (dimension 2) are
+// plane_bytes apart, or d1 rows when plane_bytes is 0.  Cached per key.
 static etree_status get_map_rows(const void* ptr, int rank, uint64_t d0, uint64_t d1, uint64_t d2,
                                  uint64_t row_bytes, uint32_t b0, uint32_t b1, uint32_t b2,
-                                 CUtensorMap* out) {
+                                 CUtensorMap* out, uint64_t plane_bytes = 0) {
   int dev = 0;
   cudaGetDevice(&dev);
-  MapKey key{reinterpret_cast<uintptr_t>(ptr), d0, d1, d2, row_bytes, b0, b1, b2,
+  MapKey key{reinterpret_cast<uintptr_t>(ptr), d0, d1, d2, row_bytes, plane_bytes, b0, b1, b2,
              (uint32_t)rank, dev};
   {
     std::lock_guard<std::mutex> lk(g_map_mu);
@@ -189,7 +191,7 @@ static etree_status get_map_rows(const void* ptr, int rank, uint64_t d0, uint64_
   if (!fn) return fail(ETREE_ECUDA, "cuTensorMapEncodeTiled is unavailable");
   cuuint64_t dims[3] = {d0, d1, d2};
   const uint64_t rb = row_bytes ? row_bytes : d0 * 2;
-  cuuint64_t strides[2] = {rb, rb * d1};
+  cuuint64_t strides[2] = {rb, plane_bytes ? plane_bytes : rb * d1};
   cuuint32_t box[3] = {b0, b1, b2};
   cuuint32_t estr[3] = {1, 1, 1};
   CUtensorMap m;
@@ -660,6 +662,178 @@ etree_status etree_verify_attn_paged(const etree_batch* b, const int32_t* block_
   if (st) return st;
   return verify_attn_impl(b, q, k_tree, v_tree, k_pool, v_pool, num_pages * page_size, hq, hkv,
                           head_dim, scale, out, lse, &pg, workspace, workspace_bytes, stream);
+}
+
+// ------------------------------------------------------------- differential tree attention
+// Launch plan: row blocks as in the ordinary attention, 64-key tiles, one CTA per SM.  The KV range
+// is split where that shortens the longest SM's work: `c` CTAs per SM in turn, each its tiles plus
+// a start of about kDiffStart tiles' time; a split also needs the merge kernel, counted as
+// kDiffMerge tiles.
+struct DiffPlan {
+  int G, nb, mchunks, nsplit, tps;
+};
+constexpr int kDiffStart = 6, kDiffMerge = 8;
+
+static DiffPlan plan_diff(const etree_batch* b, int hq, int hkv) {
+  DiffPlan pl{};
+  pl.G = hq / hkv;
+  pl.nb = std::min(128 / pl.G, b->n_max);
+  pl.mchunks = (b->n_max + pl.nb - 1) / pl.nb;
+  const int64_t pairs = (int64_t)b->B * hkv * pl.mchunks;
+  const int sms = sm_count();
+  const int tiles = (int)(((int64_t)b->kv_len_max + 63) / 64) + 1;
+  int64_t best = INT64_MAX;
+  pl.tps = tiles;
+  for (int ns = 1; ns <= std::min(tiles, 2 * sms); ++ns) {
+    if (ns > 1 && pairs * ns > 4 * (int64_t)sms) break;
+    const int tps = (tiles + ns - 1) / ns;
+    const int64_t c = (pairs * ns + sms - 1) / sms;
+    const int64_t cost = c * (tps + kDiffStart) + (ns > 1 ? kDiffMerge : 0);
+    if (cost < best) {
+      best = cost;
+      pl.tps = tps;
+    }
+  }
+  pl.nsplit = (tiles + pl.tps - 1) / pl.tps;
+  return pl;
+}
+
+struct DiffLayout {
+  size_t order, o_part, ml_part, total;
+};
+
+static DiffLayout diff_layout(const etree_batch* b, const DiffPlan& pl, int hq) {
+  DiffLayout w{};
+  const size_t parts = pl.nsplit > 1 ? (size_t)b->n_total * hq * pl.nsplit * 2 : 0;
+  w.order = up256(sizeof(WsHeader));
+  w.o_part = up256(w.order + (size_t)b->B * sizeof(int32_t));
+  w.ml_part = up256(w.o_part + parts * 128 * sizeof(float));
+  w.total = up256(w.ml_part + parts * sizeof(float2));
+  return w;
+}
+
+static etree_status check_heads(int hq, int hkv) {
+  if (hq < 1 || hkv < 1 || hq % hkv != 0 || hq / hkv > 64)
+    return fail(ETREE_EINVAL, "hq=%d, hkv=%d: need hq %% hkv == 0 and hq/hkv <= 64", hq, hkv);
+  return ETREE_OK;
+}
+
+size_t etree_attn_diff_workspace_size(const etree_batch* batch, int hq, int hkv) {
+  if (check_batch(batch) != ETREE_OK || check_heads(hq, hkv) != ETREE_OK) return 0;
+  return diff_layout(batch, plan_diff(batch, hq, hkv), hq).total;
+}
+
+static etree_status attn_diff_impl(const etree_batch* b, const uint16_t* q, int64_t q_stride,
+                                   const uint16_t* k_tree, int64_t k_stride,
+                                   const uint16_t* v_tree, int64_t v_stride,
+                                   const uint16_t* k_cache, const uint16_t* v_cache,
+                                   int64_t cache_slots, int hq, int hkv, int head_dim, float scale,
+                                   const float* lambda, const uint16_t* norm_w, float norm_eps,
+                                   float out_scale, uint16_t* out, float* lse, const PagedArgs* pg,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+  etree_status st = check_attn_args(b, q, k_tree, v_tree, k_cache, v_cache, cache_slots, hq, hkv,
+                                    head_dim, scale, out, lse);
+  if (st) return st;
+  if (!(scale > 0.f)) return fail(ETREE_EINVAL, "scale must be positive");
+  if (!lambda || ((uintptr_t)lambda & 3)) return fail(ETREE_EINVAL, "lambda is NULL or misaligned");
+  if (!aligned16(norm_w)) return fail(ETREE_EINVAL, "norm_w must be 16-byte aligned");
+  if (!std::isfinite(norm_eps) || norm_eps < 0.f || !std::isfinite(out_scale))
+    return fail(ETREE_EINVAL, "norm_eps must be finite and >= 0, out_scale finite");
+  const struct { const char* name; int64_t stride; int heads; } rows[] = {
+      {"q_stride", q_stride, hq}, {"k_stride", k_stride, hkv}, {"v_stride", v_stride, hkv}};
+  for (const auto& x : rows)
+    if (x.stride < (int64_t)x.heads * head_dim || x.stride % 8 || x.stride >= (int64_t)1 << 38)
+      return fail(ETREE_EINVAL, "%s=%lld: need a multiple of 8 of at least %d heads", x.name,
+                  (long long)x.stride, x.heads);
+  if ((int64_t)b->n_total * hq > (int64_t)1 << 26 || (int64_t)b->B * hkv * b->n_max >= INT32_MAX)
+    return fail(ETREE_EINVAL, "n_total=%d with hq=%d: too many rows", b->n_total, hq);
+  const DiffPlan pl = plan_diff(b, hq, hkv);
+  const DiffLayout w = diff_layout(b, pl, hq);
+  if (!workspace || ((uintptr_t)workspace & 255))
+    return fail(ETREE_EINVAL, "workspace is NULL or not 256-byte aligned");
+  if (workspace_bytes < w.total)
+    return fail(ETREE_EINVAL, "workspace has %zu bytes, needs %zu", workspace_bytes, w.total);
+  CUtensorMap tq, kc, vc, kt, vt;
+  const uint32_t cbox = pg ? (uint32_t)std::min(64, pg->page_size) : 64;
+  if ((st = get_map(k_cache, 3, 128, hkv, cache_slots, 64, 1, cbox, &kc))) return st;
+  if ((st = get_map(v_cache, 3, 128, hkv, cache_slots, 64, 1, cbox, &vc))) return st;
+  if ((st = get_map_rows(k_tree, 3, 128, hkv, b->n_total, 256, 64, 1, 64, &kt, k_stride * 2)))
+    return st;
+  if ((st = get_map_rows(v_tree, 3, 128, hkv, b->n_total, 256, 64, 1, 64, &vt, v_stride * 2)))
+    return st;
+  if ((st = get_map_rows(q, 3, 128, hq, b->n_total, 256, 64, pl.G, pl.nb, &tq, q_stride * 2)))
+    return st;
+  DiffParams p{};
+  p.cu_nodes = b->cu_nodes;
+  p.parent = b->parent;
+  p.kv_len = b->kv_len;
+  p.slot_base = b->slot_base;
+  p.v_tree = v_tree;
+  p.v_stride = v_stride;
+  p.lambda = lambda;
+  p.norm_w = norm_w;
+  p.norm_eps = norm_eps;
+  p.out_scale = out_scale;
+  p.out = reinterpret_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.o_part = at<float>(workspace, w.o_part);
+  p.ml_part = at<float2>(workspace, w.ml_part);
+  p.ws = at<WsHeader>(workspace, 0);
+  p.cache_slots = cache_slots;
+  p.B = b->B;
+  p.n_total = b->n_total;
+  p.hq = hq;
+  p.hkv = hkv;
+  p.G = pl.G;
+  p.n_max = b->n_max;
+  p.kv_len_max = b->kv_len_max;
+  p.nb = pl.nb;
+  p.mchunks = pl.mchunks;
+  p.nsplit = pl.nsplit;
+  p.tps = pl.tps;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.block_table = pg ? pg->block_table : nullptr;
+  p.max_pages = pg ? pg->max_pages : 0;
+  p.page_shift = pg ? log2i(pg->page_size) : 0;
+  p.cache_box = (int)cbox;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (b->B >= 8) {                             // mixed lengths: the longest requests start first
+    int32_t* order = at<int32_t>(workspace, w.order);
+    p.order = order;
+    e = launch_attn_order(b->kv_len, b->B, order, s);
+    if (e != cudaSuccess) return cuda_fail(e, "etree_verify_attn_diff order");
+  }
+  e = launch_attn_diff(tq, kc, vc, kt, vt, p, s);
+  return e == cudaSuccess ? ETREE_OK : cuda_fail(e, "etree_verify_attn_diff launch");
+}
+
+etree_status etree_verify_attn_diff(const etree_batch* b, const uint16_t* q, int64_t q_stride,
+                                    const uint16_t* k_tree, int64_t k_stride,
+                                    const uint16_t* v_tree, int64_t v_stride,
+                                    const uint16_t* k_cache, const uint16_t* v_cache,
+                                    int64_t cache_slots, int hq, int hkv, int head_dim,
+                                    float scale, const float* lambda, const uint16_t* norm_w,
+                                    float norm_eps, float out_scale, uint16_t* out, float* lse,
+                                    void* workspace, size_t workspace_bytes, void* stream) {
+  return attn_diff_impl(b, q, q_stride, k_tree, k_stride, v_tree, v_stride, k_cache, v_cache,
+                        cache_slots, hq, hkv, head_dim, scale, lambda, norm_w, norm_eps, out_scale,
+                        out, lse, nullptr, workspace, workspace_bytes, stream);
+}
+
+etree_status etree_verify_attn_diff_paged(
+    const etree_batch* b, const int32_t* block_table, int32_t max_pages, int32_t page_size,
+    const uint16_t* q, int64_t q_stride, const uint16_t* k_tree, int64_t k_stride,
+    const uint16_t* v_tree, int64_t v_stride, const uint16_t* k_pool, const uint16_t* v_pool,
+    int64_t num_pages, int hq, int hkv, int head_dim, float scale, const float* lambda,
+    const uint16_t* norm_w, float norm_eps, float out_scale, uint16_t* out, float* lse,
+    void* workspace, size_t workspace_bytes, void* stream) {
+  const PagedArgs pg{block_table, max_pages, page_size};
+  etree_status st = check_paged(&pg, num_pages);
+  if (st) return st;
+  return attn_diff_impl(b, q, q_stride, k_tree, k_stride, v_tree, v_stride, k_pool, v_pool,
+                        num_pages * page_size, hq, hkv, head_dim, scale, lambda, norm_w, norm_eps,
+                        out_scale, out, lse, &pg, workspace, workspace_bytes, stream);
 }
 
 // The caller's logit buffer of the branching-tree sampler (etree_lmhead_accept_tree).

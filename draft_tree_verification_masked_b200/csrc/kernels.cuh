@@ -48,6 +48,31 @@ cudaError_t launch_attn_tc(const CUtensorMap& q, const CUtensorMap& kc, const CU
                            const CUtensorMap& kt, const CUtensorMap& vt, const AttnParams& p,
                            int nb, int n_total, cudaStream_t stream);
 
+// Differential tree attention (attn_diff.cu).
+struct DiffParams {
+  const int32_t* cu_nodes;
+  const int32_t* parent;
+  const int32_t* kv_len;
+  const int64_t* slot_base;
+  const uint16_t* v_tree;           // bf16 bits; rows v_stride elements apart
+  const float* lambda;              // [hq]
+  const uint16_t* norm_w;           // [128] bf16 bits, or null: no norm
+  __nv_bfloat16* out;
+  float* lse;                       // [n_total][hq][2], or null
+  float* o_part;                    // [n_total][hq][nsplit][2][128]
+  float2* ml_part;                  // [n_total][hq][nsplit][2] (maximum in log2 units, sum)
+  const int32_t* order;             // [B] requests by decreasing KV length, or null
+  WsHeader* ws;
+  int64_t v_stride, cache_slots;
+  int B, n_total, hq, hkv, G, n_max, kv_len_max, nb, mchunks, nsplit, tps;
+  float scale_log2, norm_eps, out_scale;
+  const int32_t* block_table;       // paged cache, as in AttnParams
+  int max_pages, page_shift, cache_box;
+};
+cudaError_t launch_attn_diff(const CUtensorMap& q, const CUtensorMap& kc, const CUtensorMap& vc,
+                             const CUtensorMap& kt, const CUtensorMap& vt, const DiffParams& p,
+                             cudaStream_t stream);
+
 struct GemmParams {
   int M, V, K, m_tiles, n_tiles, num_tiles, k_blocks;
   // per_cta = 1 (one row tile only): each CTA folds all its vocab tiles into one summary per

@@ -176,6 +176,44 @@ etree_status etree_verify_attn_paged(const etree_batch *batch, const int32_t *bl
                                      size_t workspace_bytes, void *stream);
 
 /*
+ * Differential tree attention: the difference of two softmax maps with a learned weight per head,
+ * for targets that attend this way.  Nodes see what they see in etree_verify_attn, and caches have
+ * its layout, so compaction and paging are unchanged.  The 128 dims of a query or key head are two
+ * halves q_1, q_2 of 64 dims, each with a map of its own over the same 128-dim values:
+ *   a_m = softmax(scale q_m k_m^T),  m = 1, 2;     d = a_1 v - lambda[h] a_2 v;
+ *   out = out_scale * d                                                     norm_w == NULL
+ *   out = out_scale * d / sqrt(mean(d^2) + norm_eps) * norm_w               otherwise (per head).
+ *   q        rows of [hq][128] bf16, q_stride elements apart (a fused projection is read in place)
+ *   k_tree   rows of [hkv][128] bf16, k_stride elements apart; v_tree, v_stride likewise.  Strides
+ *            are multiples of 8, at least a row's heads
+ *   lambda   [hq] fp32;  norm_w [128] bf16 (16-byte aligned) or NULL;  norm_eps >= 0
+ *   lse      [n_total][hq][2] fp32 log-sum-exp of each map's scaled scores; may be NULL
+ * scale must be positive.  Other arguments, limits and errors as etree_verify_attn, with a
+ * workspace of etree_attn_diff_workspace_size bytes (0 for invalid arguments).  Maxima, sums and
+ * both maps' outputs are held in fp32; probabilities are rounded to bf16 for their product with v.
+ * Infinities and NaN in keys or values that a node does not see do not reach its output.  Output
+ * rows of a request that is reported as invalid are left as they were.
+ */
+size_t etree_attn_diff_workspace_size(const etree_batch *batch, int hq, int hkv);
+etree_status etree_verify_attn_diff(const etree_batch *batch, const uint16_t *q, int64_t q_stride,
+                                    const uint16_t *k_tree, int64_t k_stride,
+                                    const uint16_t *v_tree, int64_t v_stride,
+                                    const uint16_t *k_cache, const uint16_t *v_cache,
+                                    int64_t cache_slots, int hq, int hkv, int head_dim,
+                                    float scale, const float *lambda, const uint16_t *norm_w,
+                                    float norm_eps, float out_scale, uint16_t *out, float *lse,
+                                    void *workspace, size_t workspace_bytes, void *stream);
+
+/* The same over a paged cache: block_table, page rules and errors as etree_verify_attn_paged. */
+etree_status etree_verify_attn_diff_paged(
+    const etree_batch *batch, const int32_t *block_table, int32_t max_pages, int32_t page_size,
+    const uint16_t *q, int64_t q_stride, const uint16_t *k_tree, int64_t k_stride,
+    const uint16_t *v_tree, int64_t v_stride, const uint16_t *k_pool, const uint16_t *v_pool,
+    int64_t num_pages, int hq, int hkv, int head_dim, float scale, const float *lambda,
+    const uint16_t *norm_w, float norm_eps, float out_scale, uint16_t *out, float *lse,
+    void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * LM head + acceptance.  The target keeps the longest drafted prefix consistent with its own
  * distribution and adds one token of its own after the first rejection ("Eagle-4 Released ...",
  * section "Technical Background"); at T > 0 the rule must keep the target's output distribution

@@ -77,3 +77,61 @@ def test_kv_store_refusals(L):
     _rejects(store(slots=C.c_void_p(0x200004)), -1, "aligned")
     _rejects(store(ws=None), -1, "workspace")
     assert store(n=0, slots=None, k=None, v=None) == 0       # nothing to store: no device work
+
+
+def _batch(**kw):
+    f = dict(B=2, n_total=6, n_max=4, kv_len_max=100, cu_nodes=0x100000, parent=0x200000,
+             tokens=0x300000, kv_len=0x400000, slot_base=0x500000, slot_cap=0x600000)
+    f.update(kw)
+    return et.Batch(**f)
+
+
+def test_attn_diff_refusals(L):
+    def attn(b=None, q=_p(20), qs=512, k=_p(21), ks=256, v=_p(22), vs=256, kc=_p(23), vc=_p(24),
+             slots=1000, hq=4, hkv=2, d=128, scale=0.125, lam=_p(25), w=_p(26), eps=1e-5, osc=0.2,
+             out=_p(27), lse=_p(28), ws=_p(29), wsb=1 << 30, paged=None):
+        b = _batch() if b is None else b
+        tail = (q, qs, k, ks, v, vs, kc, vc, slots, hq, hkv, d, scale, lam, w, eps, osc, out, lse,
+                ws, wsb, None)
+        if paged is not None:
+            return L.etree_verify_attn_diff_paged(C.byref(b), *paged, *tail)
+        return L.etree_verify_attn_diff(C.byref(b), *tail)
+
+    _rejects(attn(b=_batch(B=0)), -1, "B=")
+    _rejects(attn(b=_batch(n_max=65)), -1, "n_max")
+    _rejects(attn(b=_batch(n_total=1)), -1, "n_total")
+    _rejects(attn(b=_batch(parent=None)), -1, "NULL")
+    _rejects(attn(d=64), -2, "head_dim")
+    for hq, hkv in ((0, 1), (4, 0), (5, 2), (65, 1)):
+        _rejects(attn(hq=hq, hkv=hkv, qs=65 * 128), -1, "hq=")
+    for name in ("q", "k", "v", "kc", "vc", "out"):
+        _rejects(attn(**{name: None}), -1, "NULL")
+        _rejects(attn(**{name: C.c_void_p(0x900008)}), -1, "aligned")
+    _rejects(attn(lse=C.c_void_p(0x900002)), -1, "aligned")
+    _rejects(attn(lam=None), -1, "lambda")
+    _rejects(attn(w=C.c_void_p(0x900008)), -1, "norm_w")
+    for scale in (0.0, -1.0, float("nan"), float("inf")):
+        _rejects(attn(scale=scale), -1, "scale")
+    for eps in (-1e-6, float("nan"), float("inf")):
+        _rejects(attn(eps=eps), -1, "norm_eps")
+    _rejects(attn(osc=float("inf")), -1, "out_scale")
+    for bad in (504, 516, 0, -512, 1 << 40):
+        _rejects(attn(qs=bad), -1, "q_stride")
+    for bad in (248, 260):
+        _rejects(attn(ks=bad), -1, "k_stride")
+        _rejects(attn(vs=bad), -1, "v_stride")
+    for slots in (0, 1 << 31):
+        _rejects(attn(slots=slots), -1, "cache_slots")
+    _rejects(attn(ws=None), -1, "workspace")
+    _rejects(attn(ws=C.c_void_p(0x900080)), -1, "workspace")
+    need = L.etree_attn_diff_workspace_size(C.byref(_batch()), 4, 2)
+    assert need >= 256
+    _rejects(attn(wsb=need - 1), -1, "workspace")
+    for page in (0, 8, 24):
+        _rejects(attn(paged=(_p(30), 4, page)), -1, "page_size")
+    _rejects(attn(paged=(None, 4, 16)), -1, "block_table")
+    _rejects(attn(paged=(_p(30), 0, 16)), -1, "max_pages")
+    assert L.etree_attn_diff_workspace_size(C.byref(_batch(B=0)), 4, 2) == 0
+    assert L.etree_attn_diff_workspace_size(C.byref(_batch()), 5, 2) == 0
+    # a loose length bound sizes a workspace all the same
+    assert L.etree_attn_diff_workspace_size(C.byref(_batch(kv_len_max=2 ** 31 - 1)), 4, 2) > 256
