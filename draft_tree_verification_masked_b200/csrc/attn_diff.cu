@@ -261,54 +261,66 @@ attn_diff_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     }
   } else if (warp == 1) {
     // -------------------------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      const uint32_t idS = idesc_bf16_f32(128, kDKeys);
-      const uint32_t idO = idesc_bf16_f32(128, 128) | (1u << 16);   // B (V) is MN-major
-      bool ok = mbar_wait(&sh->q_full, 0);
-      tc_fence_after();
-      const uint64_t dq[2] = {smem_desc_sw128(sQ), smem_desc_sw128(sQ + 16384)};
-      auto pv = [&](int jj) -> bool {
-        const int pb = jj & 1;
-        const uint32_t ph = (jj >> 1) & 1;
-        const int t = t0 + jj;
-        const uint8_t* v0 = sKV + (jj % kDStages) * kDKV + 2 * kDBox;
-        // each map's warps clean one half of V in a tile with masked keys: both must be done
-        const bool masked = t >= nt_cache || L - t * kDKeys < kDKeys;
-        for (int m = 0; m < 2; ++m) {
-          if (!mbar_wait(&sh->p_full[m][pb], ph)) return false;
-          if (m == 0 && masked && !mbar_wait(&sh->p_full[1][pb], ph)) return false;
-          tc_fence_after();
-          const uint32_t pa = tmem + kDP + 64 * m + 32 * pb;
+    // The warp stays converged and one elected lane issues (see elect_one).
+    const uint32_t idS = idesc_bf16_f32(128, kDKeys);
+    const uint32_t idO = idesc_bf16_f32(128, 128) | (1u << 16);     // B (V) is MN-major
+    bool ok = mbar_wait(&sh->q_full, 0);
+    tc_fence_after();
+    const uint64_t dq = smem_desc_sw128(sQ), dk0 = smem_desc_sw128(sKV);
+    const uint64_t dv0 = smem_desc_sw128_mn(sKV + 2 * kDBox, kDBox);
+    auto pv = [&](int jj, int st) -> bool {
+      const int pb = jj & 1;
+      const uint32_t ph = (jj >> 1) & 1;
+      const int t = t0 + jj;
+      const uint64_t dv = dv0 + (uint64_t)(st * (kDKV >> 4));
+      // each map's warps clean one half of V in a tile with masked keys: both must be done
+      const bool masked = t >= nt_cache || L - t * kDKeys < kDKeys;
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        if (!mbar_wait(&sh->p_full[m][pb], ph)) return false;
+        if (m == 0 && masked && !mbar_wait(&sh->p_full[1][pb], ph)) return false;
+        tc_fence_after();
+        const uint32_t pa = tmem + kDP + 64 * m + 32 * pb;
+        if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < kDKeys / 16; ++k)
-            tc_mma_bf16_ts(tmem + 128 * m, pa + 8 * k, smem_desc_sw128_mn(v0 + k * 2048, kDBox),
-                           idO, (jj > 0 || k > 0) ? 1u : 0u);
+            tc_mma_bf16_ts(tmem + 128 * m, pa + 8 * k, dv + k * (2048 >> 4), idO,
+                           (jj > 0 || k > 0) ? 1u : 0u);
           tc_commit(&sh->p_free[m][pb]);
+          if (m == 1) tc_commit(&sh->kv_empty[st]);
         }
-        tc_commit(&sh->kv_empty[jj % kDStages]);
-        return true;
-      };
-      for (int j = 0; ok && j < T; ++j) {
-        const int st = j % kDStages;
-        if (!mbar_wait(&sh->kv_full[st], (j / kDStages) & 1)) { ok = false; break; }
-        const uint8_t* k0 = sKV + st * kDKV;
-        for (int m = 0; m < 2; ++m) {
-          if (j >= 1 && !mbar_wait(&sh->s_free[m], (j - 1) & 1)) { ok = false; break; }
-          tc_fence_after();
-          const uint64_t dk = smem_desc_sw128(k0 + m * kDBox);
+        __syncwarp();
+      }
+      return true;
+    };
+    int st = 0, st_prev = 0;
+    uint32_t kph = 0;
+    for (int j = 0; ok && j < T; ++j) {
+      if (!mbar_wait(&sh->kv_full[st], kph)) { ok = false; break; }
+      const uint64_t dk = dk0 + (uint64_t)(st * (kDKV >> 4));
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        if (j >= 1 && !mbar_wait(&sh->s_free[m], (j - 1) & 1)) { ok = false; break; }
+        tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            tc_mma_bf16(tmem + kDS + 64 * m, dq[m] + 2 * k, dk + 2 * k, idS, k > 0 ? 1u : 0u);
+            tc_mma_bf16(tmem + kDS + 64 * m, dq + m * (16384 >> 4) + 2 * k,
+                        dk + m * (kDBox >> 4) + 2 * k, idS, k > 0 ? 1u : 0u);
           tc_commit(&sh->s_full[m]);
         }
-        if (ok && j >= 1 && !pv(j - 1)) ok = false;
+        __syncwarp();
       }
-      if (ok && !pv(T - 1)) ok = false;
-      // every MMA issued above completes before TMEM is released
-      tc_commit(&sh->drain);
-      if (!mbar_wait(&sh->drain, 0)) ok = false;
-      if (!ok) report(p.ws, ETREE_ETIMEOUT, DET_WAIT_ATTN);
+      if (ok && j >= 1 && !pv(j - 1, st_prev)) ok = false;
+      st_prev = st;
+      if (++st == kDStages) { st = 0; kph ^= 1; }
     }
+    if (ok && !pv(T - 1, st_prev)) ok = false;
+    // every MMA issued above completes before TMEM is released
+    if (elect_one()) tc_commit(&sh->drain);
+    __syncwarp();
+    if (!mbar_wait(&sh->drain, 0)) ok = false;
+    if (!ok && lane == 0) report(p.ws, ETREE_ETIMEOUT, DET_WAIT_ATTN);
   } else {
     // ------------------------------------------------------------------- softmax warps
     const int m = (warp - 2) >> 2;                      // the map of this warp
