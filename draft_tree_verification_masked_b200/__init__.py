@@ -22,6 +22,7 @@ Entry points (same names as the C ABI in ``include/etree.h``)::
     etree_verify_attn_diff(batch, q, k_tree, v_tree, k_cache, v_cache, scale, lam, norm_w,
                            norm_eps, out_scale, out, lse, workspace)
     etree_verify_attn_diff_paged(batch, block_table, page_size, q, ...)
+    etree_w4_linear(x, wq, scales, zeros, group, bias, out, workspace)
     etree_device_status(workspace, stream=None) -> (status, detail)
 """
 from __future__ import annotations
@@ -40,7 +41,7 @@ __all__ = [
     "cost_table", "load_cost_table", "etree_lowrank_workspace_size",
     "etree_lowrank_candidates", "etree_page_plan", "etree_kv_store",
     "etree_attn_diff_workspace_size", "etree_verify_attn_diff", "etree_verify_attn_diff_paged",
-    "etree_device_status", "etree_selftest_timeout", "etree_strerror",
+    "etree_w4_workspace_size", "etree_w4_linear", "etree_device_status", "etree_selftest_timeout", "etree_strerror",
     "etree_version", "etree_attn_plan", "STATUS",
 ]
 
@@ -62,7 +63,7 @@ EXPORTS = ["etree_workspace_size", "etree_workspace_init", "etree_verify_attn",
            "etree_version", "etree_last_error", "etree_attn_plan", "etree_verify_attn_noalloc",
            "etree_selftest_timeout", "etree_page_plan", "etree_kv_store",
            "etree_attn_diff_workspace_size", "etree_verify_attn_diff",
-           "etree_verify_attn_diff_paged"]
+           "etree_verify_attn_diff_paged", "etree_w4_workspace_size", "etree_w4_linear"]
 
 
 class EtreeError(RuntimeError):
@@ -150,6 +151,11 @@ def lib():
     L.etree_verify_attn_diff.restype = C.c_int
     L.etree_verify_attn_diff_paged.argtypes = [bp, vp, i32, i32, *rows, *tail]
     L.etree_verify_attn_diff_paged.restype = C.c_int
+    L.etree_w4_workspace_size.argtypes = [C.c_int, C.c_int, C.c_int]
+    L.etree_w4_workspace_size.restype = C.c_size_t
+    L.etree_w4_linear.argtypes = [vp, i64, C.c_int, vp, vp, vp, C.c_int, C.c_int, C.c_int, vp, vp,
+                                  i64, C.c_int, vp, C.c_size_t, vp]
+    L.etree_w4_linear.restype = C.c_int
     L.etree_device_status.argtypes = [vp, vp, C.POINTER(i32)]
     L.etree_device_status.restype = C.c_int
     L.etree_selftest_timeout.argtypes = [vp, C.c_size_t, vp]
@@ -576,6 +582,51 @@ def etree_verify_attn_diff_paged(batch: Batch, block_table, page_size: int, q, k
                                     norm_eps, out_scale, out, lse, workspace),
         _stream(stream))
     return _check(st) if check else st
+
+
+def etree_w4_workspace_size(M: int, N: int, K: int) -> int:
+    return int(lib().etree_w4_workspace_size(int(M), int(N), int(K)))
+
+
+def etree_w4_linear(x, wq, scales, zeros, group: int, bias, out, workspace, stream=None,
+                    check: bool = True) -> int:
+    """x bf16 [M, K]; wq uint8 [N, K / 2], two weights a byte; scales bf16 [N, K / group]; zeros
+    uint8 [N, K / group] or None; bias bf16 [N] or None; out bf16 or fp32 [M, N].  Rows of x and
+    out may lie any stride apart."""
+    bf, u8 = torch.bfloat16, torch.uint8
+    M, K = x.shape
+    N = wq.shape[0]
+    group = int(group)
+    if out.dtype not in (bf, torch.float32):
+        raise TypeError(f"out must be bfloat16 or float32, got {out.dtype}")
+    if tuple(wq.shape) != (N, K // 2) or tuple(out.shape) != (M, N):
+        raise ValueError(f"wq and out must be [N, {K // 2}] and [{M}, N]")
+    groups = (N, K // max(1, group))
+    if tuple(scales.shape) != groups or (zeros is not None and tuple(zeros.shape) != groups):
+        raise ValueError(f"scales and zeros must be {groups}")
+    _numel(bias, N, "bias")
+    xp, xs = _matrix(x, bf, "x")
+    op, os_ = _matrix(out, out.dtype, "out")
+    _here(x, wq, scales, zeros, bias, out, workspace)
+    st = lib().etree_w4_linear(
+        xp, xs, M, _ptr(wq, u8, "wq"), _ptr(scales, bf, "scales"), _ptr(zeros, u8, "zeros"), group,
+        N, K, _ptr(bias, bf, "bias"), op, os_, int(out.dtype == torch.float32),
+        _ptr(workspace, u8, "workspace"), workspace.numel(), _stream(stream))
+    return _check(st) if check else st
+
+
+def _matrix(t, dtype, name: str):
+    """Pointer and row stride of a [rows, columns] tensor whose rows are dense inside."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on a CUDA device")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: rows must be contiguous")
+    return t.data_ptr(), (t.stride(0) if rows > 1 else cols)
 
 
 def etree_attn_plan(batch: Batch, hq: int, hkv: int) -> dict:

@@ -16,7 +16,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libetree.so")
 SOURCES = ["api.cu", "attn_combine.cu", "attn_tc.cu", "lmhead.cu", "accept.cu", "compact.cu",
-           "plan.cu", "lowrank.cu", "pages.cu", "attn_diff.cu"]
+           "plan.cu", "lowrank.cu", "pages.cu", "attn_diff.cu", "w4.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC = os.environ.get("NVCC", "nvcc")
 

@@ -214,6 +214,23 @@ static etree_status get_map(const void* ptr, int rank, uint64_t d0, uint64_t d1,
   return get_map_rows(ptr, rank, d0, d1, d2, 0, b0, b1, b2, out);
 }
 
+// Byte tensor map {row_bytes, rows} with 64-byte swizzle and boxes of 64 bytes x 128 rows: packed
+// 4-bit weights.  Not cached: encoded per call.
+static etree_status get_map_w4(const void* ptr, uint64_t row_bytes, uint64_t rows,
+                               CUtensorMap* out) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return fail(ETREE_ECUDA, "cuTensorMapEncodeTiled is unavailable");
+  cuuint64_t dims[2] = {row_bytes, rows};
+  cuuint64_t strides[1] = {row_bytes};
+  cuuint32_t box[2] = {64, 128};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = fn(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box,
+                  estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(ETREE_ECUDA, "cuTensorMapEncodeTiled (bytes) failed (%d)", (int)r);
+  return ETREE_OK;
+}
+
 // fp32 2-D tensor map {d0 (contiguous), d1} with row stride d0 * 4 bytes and 64-byte swizzle, for
 // the TMA stores of materialised logit rows (box {b0, b1}).  Not cached: encoded per call.
 static etree_status get_map_f32_sw64(const void* ptr, uint64_t d0, uint64_t d1, uint32_t b0,
@@ -834,6 +851,103 @@ etree_status etree_verify_attn_diff_paged(
   return attn_diff_impl(b, q, q_stride, k_tree, k_stride, v_tree, v_stride, k_pool, v_pool,
                         num_pages * page_size, hq, hkv, head_dim, scale, lambda, norm_w, norm_eps,
                         out_scale, out, lse, &pg, workspace, workspace_bytes, stream);
+}
+
+// ------------------------------------------------------------------ products with 4-bit weights
+struct W4Plan {
+  int nt, ks, chunks, kbu, tiles, grid;
+  int64_t units;
+  size_t count, xp, part, total;
+};
+
+// Tokens go in chunks of 16, 32 or 64.  Units of four row tiles read x once for 512 rows and are
+// taken where they fill the SMs; with fewer rows a unit is four k blocks of one row tile.
+static W4Plan plan_w4(int M, int N, int K) {
+  W4Plan pl{};
+  const int sms = sm_count();
+  pl.nt = M <= 16 ? 16 : M <= 32 ? 32 : 64;
+  pl.chunks = (M + pl.nt - 1) / pl.nt;
+  const int nkb = (K + 127) / 128;
+  pl.ks = (int64_t)((N + 511) / 512) * pl.chunks * 2 >= sms ? 1 : 4;
+  const int rpt = pl.ks == 4 ? 128 : 512;
+  pl.kbu = (nkb + pl.ks - 1) / pl.ks;
+  pl.tiles = (N + rpt - 1) / rpt * pl.chunks;
+  pl.units = (int64_t)pl.tiles * pl.kbu;
+  pl.grid = (int)std::min<int64_t>(pl.units, sms);
+  pl.count = up256(sizeof(WsHeader));
+  pl.xp = up256(pl.count + (size_t)pl.tiles * sizeof(int32_t));
+  pl.part = up256(pl.xp + (size_t)pl.chunks * pl.nt * K * 2);
+  pl.total = up256(pl.part + (size_t)2 * pl.grid * pl.nt * rpt * sizeof(float));
+  return pl;
+}
+
+static etree_status check_w4(int M, int N, int K) {
+  if (M < 0 || M > 65536) return fail(ETREE_EINVAL, "M=%d outside [0, 65536]", M);
+  if (N < 1 || N > (1 << 24)) return fail(ETREE_EINVAL, "N=%d outside [1, 2^24]", N);
+  if (K < 32 || K > (1 << 18) || K % 32)
+    return fail(ETREE_EINVAL, "K=%d: need a multiple of 32 in [32, 2^18]", K);
+  return ETREE_OK;
+}
+
+size_t etree_w4_workspace_size(int M, int N, int K) {
+  if (check_w4(M, N, K) != ETREE_OK) return 0;
+  return plan_w4(std::max(M, 1), N, K).total;
+}
+
+etree_status etree_w4_linear(const uint16_t* x, int64_t x_stride, int M, const uint8_t* wq,
+                             const uint16_t* scales, const uint8_t* zeros, int group, int N, int K,
+                             const uint16_t* bias, void* out, int64_t out_stride, int out_f32,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+  etree_status st = check_w4(M, N, K);
+  if (st) return st;
+  if ((group != 32 && group != 64 && group != 128) || K % group)
+    return fail(ETREE_EINVAL, "group=%d: need 32, 64 or 128, a divisor of K=%d", group, K);
+  if (out_f32 != 0 && out_f32 != 1) return fail(ETREE_EINVAL, "out_f32=%d", out_f32);
+  if (M == 0) return ETREE_OK;
+  if (!x || !wq || !scales || !out) return fail(ETREE_EINVAL, "a tensor pointer is NULL");
+  if (!aligned16(x) || !aligned16(wq) || !aligned16(scales) || !aligned16(zeros))
+    return fail(ETREE_EINVAL, "x and the weights must be 16-byte aligned");
+  if (((uintptr_t)out & (out_f32 ? 3 : 1)) || ((uintptr_t)bias & 1))
+    return fail(ETREE_EINVAL, "out or bias is misaligned");
+  if (x_stride < K || x_stride % 8 || x_stride >= (int64_t)1 << 38)
+    return fail(ETREE_EINVAL, "x_stride=%lld: need a multiple of 8 of at least K=%d",
+                (long long)x_stride, K);
+  if (out_stride < N || out_stride >= (int64_t)1 << 38)
+    return fail(ETREE_EINVAL, "out_stride=%lld: need at least N=%d", (long long)out_stride, N);
+  const W4Plan pl = plan_w4(M, N, K);
+  if (!workspace || ((uintptr_t)workspace & 255))
+    return fail(ETREE_EINVAL, "workspace is NULL or not 256-byte aligned");
+  if (workspace_bytes < pl.total)
+    return fail(ETREE_EINVAL, "workspace has %zu bytes, needs %zu", workspace_bytes, pl.total);
+  CUtensorMap tq, tx;
+  if ((st = get_map_w4(wq, K / 2, N, &tq))) return st;
+  if ((st = get_map(at<uint16_t>(workspace, pl.xp), 2, K, (uint64_t)pl.chunks * pl.nt, 1, 64,
+                    pl.nt, 1, &tx)))
+    return st;
+  W4Params p{};
+  p.x = x;
+  p.x_stride = x_stride;
+  p.scales = scales;
+  p.zeros = zeros;
+  p.bias = bias;
+  p.out = out;
+  p.out_stride = out_stride;
+  p.out_f32 = out_f32;
+  p.xp = at<uint16_t>(workspace, pl.xp);
+  p.part = at<float>(workspace, pl.part);
+  p.count = at<int32_t>(workspace, pl.count);
+  p.ws = at<WsHeader>(workspace, 0);
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.group = group;
+  p.ks = pl.ks;
+  p.kbu = pl.kbu;
+  p.chunks = pl.chunks;
+  p.tiles = pl.tiles;
+  p.units = pl.units;
+  cudaError_t e = launch_w4(tq, tx, p, pl.nt, pl.grid, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ETREE_OK : cuda_fail(e, "etree_w4_linear launch");
 }
 
 // The caller's logit buffer of the branching-tree sampler (etree_lmhead_accept_tree).

@@ -43,17 +43,17 @@ constexpr int kDBox = kDKeys * 128;         // one [64 keys][64 dims] bf16 box
 constexpr int kDKV = 4 * kDBox;             // K halves, V halves
 constexpr int kDQ = 2 * 16384;              // Q halves, [128 rows][64 dims]
 constexpr float kDLazy = 8.0f;              // rescale O only when the maximum grows by > 2^8
-// TMEM columns: O_m at 128 m, S_m at 256 + 64 m, P_m buffer b at 384 + 64 m + 32 b
-constexpr int kDS = 256, kDP = 384, kDCols = 512;
-constexpr int kDThreads = 32 * 10;
+// TMEM columns: O_m at 128 m; buffer b of map m at 256 + 128 m + 64 b: S (fp32), then P in its place
+constexpr int kDS = 256, kDCols = 512;
+constexpr int kDThreads = 32 * 12;
 
 struct DiffSmem {
-  uint64_t kv_full[kDStages], kv_empty[kDStages], q_full, drain;
-  uint64_t s_full[2], s_free[2], p_full[2][2], p_free[2][2];
+  uint64_t kv_full[kDStages], kv_empty[kDStages], q_full, drain[2];
+  uint64_t s_full[2][2], p_full[2][2], o_done[2];
   uint64_t anc[64];
   unsigned long long bad;                   // tree nodes whose V holds an infinity or NaN
   int32_t par[64];
-  float l[2][128], m[2][128], sq[2][128];   // per map: row sum, row maximum; per half: sum of d^2
+  float l[2][128], sq[2][128];              // per map: row sum; per half: sum of d^2
   uint32_t tmem;
 };
 
@@ -76,6 +76,39 @@ __device__ __forceinline__ bool bf16_nonfinite(uint32_t u) { return (u & 0x7f80u
 // a w0 + b w1, both products rounded alike (no fused multiply-add), so that equal maps cancel.
 __device__ __forceinline__ float diff2(float a, float w0, float b, float w1) {
   return __fadd_rn(__fmul_rn(a, w0), __fmul_rn(b, w1));
+}
+
+// Two fp32 words as a pair of bf16, rounded to the nearest with ties away from zero (finite values
+// and infinities; a NaN becomes a number, so its row's sum has to carry it).  Three integer
+// operations: the conversion instruction runs at the exponentials' rate and beside them.
+__device__ __forceinline__ uint32_t round_pair(uint32_t lo, uint32_t hi) {
+  return __byte_perm(lo + 0x8000u, hi + 0x8000u, 0x7632);
+}
+
+// 64 consecutive fp32 columns of this thread's TMEM lane, in one load.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
+  uint32_t r[64];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+      "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+      "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+        "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+        "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+        "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+        "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]),
+        "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]),
+        "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]),
+        "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]),
+        "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 __device__ __forceinline__ void softmax_warps_sync() {
@@ -127,16 +160,15 @@ attn_diff_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   if (threadIdx.x == 0) {
     for (int i = 0; i < kDStages; ++i) {
       mbar_init(&sh->kv_full[i], 1);
-      mbar_init(&sh->kv_empty[i], 1);
+      mbar_init(&sh->kv_empty[i], 2);
     }
     mbar_init(&sh->q_full, 1);
-    mbar_init(&sh->drain, 1);
     for (int m = 0; m < 2; ++m) {
-      mbar_init(&sh->s_full[m], 1);
-      mbar_init(&sh->s_free[m], 4);
+      mbar_init(&sh->o_done[m], 1);
+      mbar_init(&sh->drain[m], 1);
       for (int b = 0; b < 2; ++b) {
+        mbar_init(&sh->s_full[m][b], 1);
         mbar_init(&sh->p_full[m][b], 4);
-        mbar_init(&sh->p_free[m][b], 1);
       }
     }
     sh->bad = 0ull;
@@ -259,71 +291,70 @@ attn_diff_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         drained = mbar_wait(&sh->kv_full[j % kDStages], (j / kDStages) & 1) && drained;
       if (!drained) report(p.ws, ETREE_ETIMEOUT, DET_WAIT_ATTN);
     }
-  } else if (warp == 1) {
-    // -------------------------------------------------------------------------- MMA issuer
+  } else if (warp == 1 || warp == 2) {
+    // --------------------------------------------------------------- MMA issuers, one per map
     // The warp stays converged and one elected lane issues (see elect_one).
+    const int m = warp - 1;
     const uint32_t idS = idesc_bf16_f32(128, kDKeys);
     const uint32_t idO = idesc_bf16_f32(128, 128) | (1u << 16);     // B (V) is MN-major
-    bool ok = mbar_wait(&sh->q_full, 0);
-    tc_fence_after();
-    const uint64_t dq = smem_desc_sw128(sQ), dk0 = smem_desc_sw128(sKV);
+    const uint64_t dq = smem_desc_sw128(sQ + m * 16384), dk0 = smem_desc_sw128(sKV + m * kDBox);
     const uint64_t dv0 = smem_desc_sw128_mn(sKV + 2 * kDBox, kDBox);
-    auto pv = [&](int jj, int st) -> bool {
-      const int pb = jj & 1;
-      const uint32_t ph = (jj >> 1) & 1;
-      const int t = t0 + jj;
-      const uint64_t dv = dv0 + (uint64_t)(st * (kDKV >> 4));
-      // each map's warps clean one half of V in a tile with masked keys: both must be done
-      const bool masked = t >= nt_cache || L - t * kDKeys < kDKeys;
+    bool ok = mbar_wait(&sh->q_full, 0);
+    int ks = 0;                                         // the next K tile's stage and phase
+    uint32_t kph = 0;
+    auto qk = [&](int j) -> bool {
+      if (!mbar_wait(&sh->kv_full[ks], kph)) return false;
+      tc_fence_after();
+      const uint64_t dk = dk0 + (uint64_t)(ks * (kDKV >> 4));
+      if (elect_one()) {
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        if (!mbar_wait(&sh->p_full[m][pb], ph)) return false;
-        if (m == 0 && masked && !mbar_wait(&sh->p_full[1][pb], ph)) return false;
-        tc_fence_after();
-        const uint32_t pa = tmem + kDP + 64 * m + 32 * pb;
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < kDKeys / 16; ++k)
-            tc_mma_bf16_ts(tmem + 128 * m, pa + 8 * k, dv + k * (2048 >> 4), idO,
-                           (jj > 0 || k > 0) ? 1u : 0u);
-          tc_commit(&sh->p_free[m][pb]);
-          if (m == 1) tc_commit(&sh->kv_empty[st]);
-        }
-        __syncwarp();
+        for (int k = 0; k < 4; ++k)
+          tc_mma_bf16(tmem + kDS + 128 * m + 64 * (j & 1), dq + 2 * k, dk + 2 * k, idS,
+                      k > 0 ? 1u : 0u);
+        tc_commit(&sh->s_full[m][j & 1]);
       }
+      __syncwarp();
+      if (++ks == kDStages) { ks = 0; kph ^= 1; }
       return true;
     };
-    int st = 0, st_prev = 0;
-    uint32_t kph = 0;
+    ok = ok && qk(0);
+    if (T > 1) ok = ok && qk(1);
+    int vs = 0;
     for (int j = 0; ok && j < T; ++j) {
-      if (!mbar_wait(&sh->kv_full[st], kph)) { ok = false; break; }
-      const uint64_t dk = dk0 + (uint64_t)(st * (kDKV >> 4));
+      const int b = j & 1, t = t0 + j;
+      const uint32_t ph = (j >> 1) & 1;
+      // each map's warps clean one half of V in a tile with masked keys (at most the last two):
+      // both must be done
+      const bool masked = t >= nt_cache || L - t * kDKeys < kDKeys;
+      if (!mbar_wait(&sh->p_full[m][b], ph)) { ok = false; break; }
+      if (masked && !mbar_wait(&sh->p_full[1 - m][b], ph)) { ok = false; break; }
+      tc_fence_after();
+      const uint64_t dv = dv0 + (uint64_t)(vs * (kDKV >> 4));
+      const uint32_t pa = tmem + kDS + 128 * m + 64 * b;
+      if (elect_one()) {
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        if (j >= 1 && !mbar_wait(&sh->s_free[m], (j - 1) & 1)) { ok = false; break; }
-        tc_fence_after();
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc_mma_bf16(tmem + kDS + 64 * m, dq + m * (16384 >> 4) + 2 * k,
-                        dk + m * (kDBox >> 4) + 2 * k, idS, k > 0 ? 1u : 0u);
-          tc_commit(&sh->s_full[m]);
-        }
-        __syncwarp();
+        for (int k = 0; k < kDKeys / 16; ++k)
+          tc_mma_bf16_ts(tmem + 128 * m, pa + 8 * k, dv + k * (2048 >> 4), idO,
+                         (j > 0 || k > 0) ? 1u : 0u);
+        tc_commit(&sh->o_done[m]);
+        tc_commit(&sh->kv_empty[vs]);
       }
-      if (ok && j >= 1 && !pv(j - 1, st_prev)) ok = false;
-      st_prev = st;
-      if (++st == kDStages) { st = 0; kph ^= 1; }
+      __syncwarp();
+      if (++vs == kDStages) vs = 0;
+      // S of tile j + 2 takes the buffer that P of tile j was read from (and after the last tile
+      // no MMA is in flight when TMEM is released)
+      if (!mbar_wait(&sh->o_done[m], j & 1)) { ok = false; break; }
+      if (j + 2 < T) ok = qk(j + 2);
     }
-    if (ok && !pv(T - 1, st_prev)) ok = false;
-    // every MMA issued above completes before TMEM is released
-    if (elect_one()) tc_commit(&sh->drain);
-    __syncwarp();
-    if (!mbar_wait(&sh->drain, 0)) ok = false;
-    if (!ok && lane == 0) report(p.ws, ETREE_ETIMEOUT, DET_WAIT_ATTN);
-  } else {
+    if (!ok) {                                          // what was issued ends before TMEM goes
+      if (elect_one()) tc_commit(&sh->drain[m]);
+      __syncwarp();
+      mbar_wait(&sh->drain[m], 0);
+      if (lane == 0) report(p.ws, ETREE_ETIMEOUT, DET_WAIT_ATTN);
+    }
+  } else if (warp >= 4) {
     // ------------------------------------------------------------------- softmax warps
-    const int m = (warp - 2) >> 2;                      // the map of this warp
+    const int m = (warp - 4) >> 2;                      // the map of this warp
     const int wq = warp & 3;                            // its TMEM lane quarter
     const int row = wq * 32 + lane;
     const int node_l = row / G, g = row - node_l * G;
@@ -337,16 +368,11 @@ attn_diff_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     bool ok = true;
     for (int j = 0; j < T; ++j) {
       const int t = t0 + j;
-      if (!mbar_wait(&sh->s_full[m], j & 1)) { ok = false; break; }
+      const uint32_t buf = lane_base + kDS + 128 * m + 64 * (j & 1);
+      if (!mbar_wait(&sh->s_full[m][j & 1], (j >> 1) & 1)) { ok = false; break; }
       tc_fence_after();
       float sc[64];
-      if (work) {
-        tmem_ld32(lane_base + kDS + 64 * m, *reinterpret_cast<float(*)[32]>(sc));
-        tmem_ld32(lane_base + kDS + 64 * m + 32, *reinterpret_cast<float(*)[32]>(sc + 32));
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->s_free[m]);
+      if (work) tmem_ld64(buf, sc);
 
       const int lim = t < nt_cache ? min(kDKeys, L - t * kDKeys) : n;   // rows of the tile in use
       const bool masked = t >= nt_cache || lim < kDKeys;
@@ -356,7 +382,7 @@ attn_diff_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         uint8_t* v = sKV + (j % kDStages) * kDKV + (2 + m) * kDBox;
         unsigned long long bad = 0ull;
 #pragma unroll 1
-        for (int c = row; c < kDKeys * 8; c += 128) {   // 16-byte chunks; a row is 8 of them
+        for (int c = row; c < kDKeys * 8; c += 128) {   // 16-byte chunks, 8 a row
           uint4* at = reinterpret_cast<uint4*>(v + c * 16);
           const int key = c >> 3;
           if (key >= lim) {
@@ -379,7 +405,6 @@ attn_diff_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         if (bad) atomicOr(&sh->bad, bad);
         fence_proxy_async();
       }
-      const int pb = j & 1;
       if (work) {
         if (masked) {
           uint64_t kw;                                  // bit c: key c of the tile is visible
@@ -411,15 +436,17 @@ attn_diff_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           const float e2 = ex2_approx(x2), e3 = ex2_approx(x3);
           fadd2(a0, a1, e0, e1);
           fadd2(a0, a1, e2, e3);
-          pk[c] = __uint_as_float(pack_bf16x2(e0, e1));
-          pk[c + 1] = __uint_as_float(pack_bf16x2(e2, e3));
+          const uint32_t u[4] = {__float_as_uint(e0), __float_as_uint(e1), __float_as_uint(e2),
+                                 __float_as_uint(e3)};
+          pk[c] = __uint_as_float(round_pair(u[0], u[1]));
+          pk[c + 1] = __uint_as_float(round_pair(u[2], u[3]));
         }
         const float corr = need ? ex2_approx(m_ref - m_new) : 1.f;
         l = l * corr + (a0 + a1);
         m_ref = m_new;
         // A rescale of O_m needs every earlier product of this map finished (the last wrote O_m).
         if (any && j >= 1) {
-          if (!mbar_wait(&sh->p_free[m][(j - 1) & 1], ((j - 1) >> 1) & 1)) { ok = false; break; }
+          if (!mbar_wait(&sh->o_done[m], (j - 1) & 1)) { ok = false; break; }
           tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
@@ -431,24 +458,18 @@ attn_diff_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             tmem_st32(ta, o);
           }
         }
-        // P_m buffer j % 2 is free once the product of tile j - 2 has completed
-        if (j >= 2) {
-          if (!mbar_wait(&sh->p_free[m][pb], ((j >> 1) & 1) ^ 1)) { ok = false; break; }
-          tc_fence_after();
-        }
-        tmem_st32(lane_base + kDP + 64 * m + 32 * pb, pk);
+        tmem_st32(buf, pk);
         tc_fence_before();
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->p_full[m][pb]);
+      if (lane == 0) mbar_arrive(&sh->p_full[m][j & 1]);
     }
-    if (ok && !mbar_wait(&sh->p_free[m][(T - 1) & 1], ((T - 1) >> 1) & 1)) ok = false;
+    if (ok && !mbar_wait(&sh->o_done[m], (T - 1) & 1)) ok = false;
     if (!ok) report(p.ws, ETREE_ETIMEOUT, DET_WAIT_ATTN);
     tc_fence_after();
     const int h = kvh * G + g;
     const size_t gidx = (size_t)(base + (valid ? node : 0)) * p.hq + (valid ? h : 0);
     sh->l[m][row] = l;
-    sh->m[m][row] = m_ref;
     softmax_warps_sync();                               // both maps' O, sums and `bad` are final
     tc_fence_after();
     // columns [c0, c0 + 32) of O_mm, with the values taken out of the tree tile put back

@@ -214,4 +214,23 @@ struct StoreParams {
 };
 cudaError_t launch_kv_store(const StoreParams& p, cudaStream_t s);
 
+// Products with 4-bit weights (w4.cu).
+struct W4Params {
+  const uint16_t* x;                // bf16 bits, rows x_stride elements apart
+  const uint16_t* scales;           // [N][K / group] bf16 bits
+  const uint8_t* zeros;             // [N][K / group], or null: 8
+  const uint16_t* bias;             // [N] bf16 bits, or null
+  void* out;                        // bf16 or fp32, rows out_stride elements apart
+  uint16_t* xp;                     // workspace: x in the kernel's order, [chunks * NT][K]
+  float* part;                      // workspace: two partial tiles a CTA
+  int32_t* count;                   // workspace: per tile, the CTAs that delivered their part
+  WsHeader* ws;
+  int64_t x_stride, out_stride, units;
+  int M, N, K, group, out_f32;
+  int ks, kbu, chunks, tiles, stages;   // k blocks a unit; units a tile; token chunks; tiles
+};
+int w4_stages(int nt, int ks);
+cudaError_t launch_w4(const CUtensorMap& q, const CUtensorMap& x, W4Params p, int nt, int grid,
+                      cudaStream_t s);
+
 }  // namespace etree

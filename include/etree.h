@@ -214,6 +214,27 @@ etree_status etree_verify_attn_diff_paged(
     void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * Products with 4-bit weights and group scales: projections of a target held in 4 bits, and its
+ * vocabulary projection, over the nodes of a step.
+ *   out[m][n] = bias[n] + sum_k x[m][k] * (q[n][k] - zeros[n][k / group]) * scales[n][k / group]
+ *   x        [M] rows of K bf16, x_stride elements apart (a multiple of 8, at least K)
+ *   wq       [N][K / 2]: byte k / 2 of a row holds q[k] in its low and q[k + 1] in its high half
+ *   scales   [N][K / group] bf16;  zeros [N][K / group], one byte each (its low four bits are
+ *            read), or NULL: 8 throughout;  group 32, 64 or 128, a divisor of K
+ *   bias     [N] bf16 or NULL
+ *   out      [M] rows of N bf16 (out_f32 = 0) or fp32 (1), out_stride elements apart, at least N
+ * x, wq, scales and zeros are 16-byte aligned; K is a multiple of 32 up to 2^18, 0 <= M <= 65536.
+ * No weight is rounded: products with the integers q - zeros are exact and added in fp32, group by
+ * group, times the scale.  Results do not depend on timing.  out may not overlap an input.
+ * Two launches; the workspace has etree_w4_workspace_size bytes (0 for invalid arguments).
+ */
+size_t etree_w4_workspace_size(int M, int N, int K);
+etree_status etree_w4_linear(const uint16_t* x, int64_t x_stride, int M, const uint8_t* wq,
+                             const uint16_t* scales, const uint8_t* zeros, int group, int N, int K,
+                             const uint16_t* bias, void* out, int64_t out_stride, int out_f32,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * LM head + acceptance.  The target keeps the longest drafted prefix consistent with its own
  * distribution and adds one token of its own after the first rejection ("Eagle-4 Released ...",
  * section "Technical Background"); at T > 0 the rule must keep the target's output distribution

@@ -135,3 +135,38 @@ def test_attn_diff_refusals(L):
     assert L.etree_attn_diff_workspace_size(C.byref(_batch()), 5, 2) == 0
     # a loose length bound sizes a workspace all the same
     assert L.etree_attn_diff_workspace_size(C.byref(_batch(kv_len_max=2 ** 31 - 1)), 4, 2) > 256
+
+
+def test_w4_refusals(L):
+    def lin(x=_p(1), xs=256, M=4, wq=_p(2), s=_p(3), z=_p(4), group=64, N=100, K=256, b=_p(5),
+            out=_p(6), os=100, f32=0, ws=_p(7), wsb=1 << 30):
+        return L.etree_w4_linear(x, xs, M, wq, s, z, group, N, K, b, out, os, f32, ws, wsb, None)
+
+    for M in (-1, 65537):
+        _rejects(lin(M=M), -1, "M=")
+    for N in (0, (1 << 24) + 1):
+        _rejects(lin(N=N, os=1 << 25), -1, "N=")
+    for K in (0, 16, 250, 1 << 19):
+        _rejects(lin(K=K, xs=1 << 20), -1, "K=")
+    for group in (0, 16, 96, 256):
+        _rejects(lin(group=group), -1, "group")
+    _rejects(lin(group=128, K=320, xs=320), -1, "group")
+    _rejects(lin(f32=2), -1, "out_f32")
+    for name in ("x", "wq", "s", "out"):
+        _rejects(lin(**{name: None}), -1, "NULL")
+    for name in ("x", "wq", "s", "z"):
+        _rejects(lin(**{name: C.c_void_p(0x900008)}), -1, "aligned")
+    _rejects(lin(out=C.c_void_p(0x900002), f32=1), -1, "misaligned")
+    _rejects(lin(out=C.c_void_p(0x900001)), -1, "misaligned")
+    _rejects(lin(b=C.c_void_p(0x900001)), -1, "misaligned")
+    for xs in (248, 260, 0, 1 << 40):
+        _rejects(lin(xs=xs), -1, "x_stride")
+    for os in (99, 0, 1 << 40):
+        _rejects(lin(os=os), -1, "out_stride")
+    _rejects(lin(ws=None), -1, "workspace")
+    _rejects(lin(ws=C.c_void_p(0x900080)), -1, "workspace")
+    need = L.etree_w4_workspace_size(4, 100, 256)
+    assert need > 256
+    _rejects(lin(wsb=need - 1), -1, "workspace")
+    assert L.etree_w4_workspace_size(4, 0, 256) == 0 and L.etree_w4_workspace_size(4, 100, 250) == 0
+    assert lin(M=0, x=None, out=None) == 0                   # no tokens: no device work
