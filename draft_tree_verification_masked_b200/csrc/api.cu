@@ -860,16 +860,16 @@ struct W4Plan {
   size_t count, xp, part, total;
 };
 
-// Tokens go in chunks of 16, 32 or 64.  Units of four row tiles read x once for 512 rows and are
+// Tokens go in chunks of 16, 32 or 64.  Units of two row tiles read x once for 256 rows and are
 // taken where they fill the SMs; with fewer rows a unit is four k blocks of one row tile.
-static W4Plan plan_w4(int M, int N, int K) {
+static W4Plan plan_w4(int M, int N, int K) {          // checked arguments: units fit 32 bits
   W4Plan pl{};
   const int sms = sm_count();
   pl.nt = M <= 16 ? 16 : M <= 32 ? 32 : 64;
   pl.chunks = (M + pl.nt - 1) / pl.nt;
   const int nkb = (K + 127) / 128;
-  pl.ks = (int64_t)((N + 511) / 512) * pl.chunks * 2 >= sms ? 1 : 4;
-  const int rpt = pl.ks == 4 ? 128 : 512;
+  pl.ks = (int64_t)((N + 255) / 256) * pl.chunks >= sms ? 2 : 4;
+  const int rpt = pl.ks == 4 ? 128 : 256;
   pl.kbu = (nkb + pl.ks - 1) / pl.ks;
   pl.tiles = (N + rpt - 1) / rpt * pl.chunks;
   pl.units = (int64_t)pl.tiles * pl.kbu;
@@ -886,6 +886,8 @@ static etree_status check_w4(int M, int N, int K) {
   if (N < 1 || N > (1 << 24)) return fail(ETREE_EINVAL, "N=%d outside [1, 2^24]", N);
   if (K < 32 || K > (1 << 18) || K % 32)
     return fail(ETREE_EINVAL, "K=%d: need a multiple of 32 in [32, 2^18]", K);
+  if (((int64_t)M + 15) / 16 * ((N + 127) / 128) * ((K + 127) / 128) > (int64_t)1 << 30)
+    return fail(ETREE_EINVAL, "M=%d, N=%d, K=%d: too much work for one call", M, N, K);
   return ETREE_OK;
 }
 
@@ -945,7 +947,7 @@ etree_status etree_w4_linear(const uint16_t* x, int64_t x_stride, int M, const u
   p.kbu = pl.kbu;
   p.chunks = pl.chunks;
   p.tiles = pl.tiles;
-  p.units = pl.units;
+  p.units = (int)pl.units;
   cudaError_t e = launch_w4(tq, tx, p, pl.nt, pl.grid, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ETREE_OK : cuda_fail(e, "etree_w4_linear launch");
 }

@@ -225,8 +225,8 @@ struct W4Params {
   float* part;                      // workspace: two partial tiles a CTA
   int32_t* count;                   // workspace: per tile, the CTAs that delivered their part
   WsHeader* ws;
-  int64_t x_stride, out_stride, units;
-  int M, N, K, group, out_f32;
+  int64_t x_stride, out_stride;
+  int M, N, K, group, out_f32, units;
   int ks, kbu, chunks, tiles, stages;   // k blocks a unit; units a tile; token chunks; tiles
 };
 int w4_stages(int nt, int ks);

@@ -19,9 +19,9 @@
 //   D = A x^T   tcgen05.mma M=128 x N=NT x K=16, A from TMEM, x from shared memory.
 //
 // One CTA per SM walks its equal share of a flat list of work units, so that any N and K fill all
-// SMs.  A unit is four 128 x 128 weight blocks, one for each warpgroup: four row tiles at one k
-// block where there are many rows (x is then read once for 512 rows), or four k blocks of one row
-// tile (few rows; the four sums are added in shared memory).  Row tiles whose units lie on several
+// SMs.  A unit is four 128 x 128 weight blocks: two row tiles of two
+// k blocks where there are many rows (x is then read once for 256 rows), or four k blocks of one
+// row tile (few rows).  Row tiles whose units lie on several
 // CTAs are summed from partials in the workspace by the CTA that arrives last, in the order of k,
 // so results do not depend on timing.
 #include <algorithm>
@@ -31,7 +31,7 @@
 namespace etree {
 
 namespace {
-constexpr int kWThreads = 32 * 20;          // TMA, MMA, two idle, sixteen consumer warps
+constexpr int kWThreads = 32 * 12;          // TMA, MMA, two idle, eight consumer warps
 constexpr int kWBox = 128 * 64;             // [128 rows][64 bytes]
 constexpr int kWMaxStages = 5;
 constexpr int kWSmem = 220 * 1024;
@@ -43,15 +43,34 @@ struct W4Smem {
   int last;
 };
 
-__device__ __forceinline__ void w4_sync() { asm volatile("bar.sync 1, 512;" ::: "memory"); }
+__device__ __forceinline__ void w4_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 // First unit of CTA c, and the CTA that holds unit u.
-__host__ __device__ __forceinline__ long long w4_first(long long units, int grid, int c) {
-  return units * c / grid;
+__device__ __forceinline__ int w4_first(int units, int grid, int c) {
+  return (int)((int64_t)units * c / grid);
 }
-__device__ __forceinline__ int w4_owner(long long units, int grid, long long u) {
-  return (int)(((u + 1) * grid - 1) / units);
+__device__ __forceinline__ int w4_owner(int units, int grid, int u) {
+  return (int)(((int64_t)(u + 1) * grid - 1) / units);
 }
+
+// A CTA's walk over its units: the tile, its row and token chunk, and the unit's place in depth.
+struct W4Walk {
+  int tile, kb, rowt, chunk;
+  __device__ __forceinline__ W4Walk(const W4Params& p, int u) {
+    tile = u / p.kbu;
+    kb = u - tile * p.kbu;
+    rowt = tile / p.chunks;
+    chunk = tile - rowt * p.chunks;
+  }
+  __device__ __forceinline__ void next(const W4Params& p) {
+    if (++kb < p.kbu) return;
+    kb = 0;
+    ++tile;
+    if (++chunk < p.chunks) return;
+    chunk = 0;
+    ++rowt;
+  }
+};
 
 __device__ __forceinline__ void tmem_st16_async(uint32_t taddr, const uint32_t (&v)[16]) {
   asm volatile(
@@ -67,6 +86,16 @@ __device__ __forceinline__ uint32_t sub_pair(uint32_t a, uint32_t b) {
   const __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&a),
                                    *reinterpret_cast<__nv_bfloat162*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// (a0, a1) += (v0, v1) s
+__device__ __forceinline__ void ffma2_acc(float& a0, float& a1, float v0, float v1, float s) {
+  uint64_t x, ss, a;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(v0), "f"(v1));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(ss) : "f"(s));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(a0), "f"(a1));
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(a) : "l"(x), "l"(ss));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a0), "=f"(a1) : "l"(a));
 }
 
 // Scales and zero points of four consecutive groups of one row.
@@ -95,7 +124,7 @@ __global__ void __launch_bounds__(256) w4_prepare_kernel(W4Params p, int rows) {
   reinterpret_cast<uint4*>(p.xp)[i] = v;
 }
 
-template <int NT>
+template <int NT, int KS>
 __global__ void __launch_bounds__(kWThreads, 1)
 w4_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_x,
           W4Params p) {
@@ -103,21 +132,20 @@ w4_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int ks = p.ks;                                  // k blocks of a unit: 4 or 1
-  const int xbytes = NT * 256;                          // one k block of x: two boxes [NT][64]
-  const int stage = 4 * kWBox + ks * xbytes;
+  constexpr int ks = KS;                                // k blocks of a unit: 4 or 2
+  constexpr int xbytes = NT * 256;                          // one k block of x: two boxes [NT][64]
+  constexpr int stage = 4 * kWBox + ks * xbytes;
   float* red = reinterpret_cast<float*>(smem + p.stages * stage);      // [NT][128], ks = 4
   W4Smem* sh = reinterpret_cast<W4Smem*>(reinterpret_cast<uint8_t*>(red) +
                                          (ks == 4 ? NT * 128 * 4 : 0));
-  const long long u0 = w4_first(p.units, gridDim.x, blockIdx.x);
-  const long long u1 = w4_first(p.units, gridDim.x, blockIdx.x + 1);
-  const int nu = (int)(u1 - u0);
-  const int rpt = ks == 4 ? 128 : 512;                  // rows of a tile
+  const int u0 = w4_first(p.units, gridDim.x, blockIdx.x);
+  const int nu = w4_first(p.units, gridDim.x, blockIdx.x + 1) - u0;
+  constexpr int rpt = ks == 4 ? 128 : 256;                // rows of a tile
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) {
       mbar_init(&sh->full[i], 1);
-      mbar_init(&sh->empty[i], 17);
+      mbar_init(&sh->empty[i], 9);
     }
     for (int w = 0; w < 4; ++w) {
       mbar_init(&sh->a_full[w], 4);
@@ -145,40 +173,39 @@ w4_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
   if (warp == 0) {
     // ------------------------------------------------------------------------ TMA producer
     if (lane == 0) {
-      auto load_q = [&](int i) {
-        const long long u = u0 + i;
-        const int tile = (int)(u / p.kbu), kb = (int)(u % p.kbu) * ks;
-        const int row0 = tile / p.chunks * rpt;
-        uint8_t* dst = smem + (i % p.stages) * stage;
-        uint64_t* full = &sh->full[i % p.stages];
-        mbar_arrive_expect_tx(full, stage);
+      auto load_q = [&](const W4Walk& at, int st) {
+        const int kb = at.kb * ks, row0 = at.rowt * rpt;
+        uint8_t* dst = smem + st * stage;
+        mbar_arrive_expect_tx(&sh->full[st], stage);
+#pragma unroll
         for (int w = 0; w < 4; ++w)
-          tma_load_2d(dst + w * kWBox, &tm_q, full, (ks == 4 ? kb + w : kb) * 64,
-                      ks == 4 ? row0 : row0 + w * 128);
+          tma_load_2d(dst + w * kWBox, &tm_q, &sh->full[st], (kb + w % ks) * 64,
+                      row0 + w / ks * 128);
       };
-      auto load_x = [&](int i) {
-        const long long u = u0 + i;
-        const int tile = (int)(u / p.kbu), kb = (int)(u % p.kbu) * ks;
-        const int m0 = tile % p.chunks * NT;
-        uint8_t* dst = smem + (i % p.stages) * stage + 4 * kWBox;
-        uint64_t* full = &sh->full[i % p.stages];
+      auto load_x = [&](const W4Walk& at, int st) {
+        uint8_t* dst = smem + st * stage + 4 * kWBox;
         for (int w = 0; w < ks; ++w)
           for (int h = 0; h < 2; ++h)
-            tma_load_2d(dst + w * xbytes + h * (NT * 128), &tm_x, full, (kb + w) * 128 + h * 64, m0);
+            tma_load_2d(dst + w * xbytes + h * (NT * 128), &tm_x, &sh->full[st],
+                        (at.kb * ks + w) * 128 + h * 64, at.chunk * NT);
       };
       // the first weights do not depend on the kernel that reorders x
       const int ahead = min(nu, p.stages);
-      for (int i = 0; i < ahead; ++i) load_q(i);
+      W4Walk at(p, u0);
+      for (int i = 0; i < ahead; ++i, at.next(p)) load_q(at, i);
       pdl_wait();
       bool ok = true;
-      int issued = 0;
-      for (int i = 0; i < nu; ++i) {
+      int issued = 0, st = 0;
+      uint32_t ph = 0;
+      at = W4Walk(p, u0);
+      for (int i = 0; i < nu; ++i, at.next(p)) {
         if (i >= ahead) {
-          if (!mbar_wait(&sh->empty[i % p.stages], ((i / p.stages) & 1) ^ 1)) { ok = false; break; }
-          load_q(i);
+          if (!mbar_wait(&sh->empty[st], ph ^ 1)) { ok = false; break; }
+          load_q(at, st);
         }
-        load_x(i);
+        load_x(at, st);
         issued = i + 1;
+        if (++st == p.stages) { st = 0; ph ^= 1; }
       }
       // every copy has landed before the CTA may exit (bounded)
       for (int i = max(0, issued - p.stages); i < issued; ++i)
@@ -201,7 +228,7 @@ w4_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
         for (int w = 0; ok && w < 4; ++w) {
           ok = rd == 0 ? mbar_wait(&sh->a_full[w], i & 1) : mbar_wait(&sh->d_free[w], dph);
           tc_fence_after();
-          const uint64_t dxw = dx + (ks == 4 ? w * (xbytes >> 4) : 0);
+          const uint64_t dxw = dx + w % ks * (xbytes >> 4);
           if (ok && elect_one()) {
             for (int g = 0; g < per_round; ++g) {
               const uint32_t d = tmem + 256 + 64 * w + NT * g;
@@ -225,16 +252,20 @@ w4_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
     if (!ok && lane == 0) report(p.ws, ETREE_ETIMEOUT, DET_WAIT_W4);
   } else if (warp >= 4) {
     // ------------------------------------------- consumers: q to A, and the scaled group sums
-    const int w = (warp - 4) >> 2, quarter = warp & 3;
+    // A warpgroup serves two of the unit's four blocks: the tensor core works on one while the
+    // other is unpacked or read back.
+    const int wg = (warp - 4) >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
-    const uint32_t la = tmem + ((uint32_t)(quarter * 32) << 16) + 64 * w, ld = la + 256;
+    const uint32_t la = tmem + ((uint32_t)(quarter * 32) << 16) + 128 * wg, ld = la + 256;
     const int ng = p.K / p.group;
     const bool wide = (ng & 3) == 0;
+    constexpr int kLd = NT == 16 ? 16 : 32;
+    const int wrow = ks == 4 ? 0 : wg * 128;            // this warpgroup's rows in the tile
     float acc[NT];
     bool ok = true;
     int st = 0;
     uint32_t ph = 0, dph = 0;
-    W4Groups cur{0u, 0u, 0u}, nxt{0u, 0u, 0u};
+    W4Groups cur[2], nxt[2];
     auto fetch = [&](int n, int chunk) -> W4Groups {    // groups [4 chunk, 4 chunk + 4)
       W4Groups r{0u, 0u, 0x08080808u};
       if (n >= p.N || 4 * chunk >= ng) return r;
@@ -258,108 +289,120 @@ w4_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
       }
       return r;
     };
-    auto scale_of = [&](int g) -> float {               // group g of the block's chunk
-      const uint32_t v = (g & 2) ? cur.s23 : cur.s01;
-      return __uint_as_float((g & 1) ? (v & 0xffff0000u) : (v << 16));
-    };
-    auto kblock = [&](long long u) { return (int)(u % p.kbu) * ks + (ks == 4 ? w : 0); };
-    auto nrow = [&](long long u) {
-      return (int)(u / p.kbu) / p.chunks * rpt + (ks == 4 ? 0 : w * 128) + row;
-    };
-    long long have = -1;                                // the chunk in `cur`, as n-tile and index
-    if (nu > 0) nxt = fetch(nrow(u0), kblock(u0) * gpb >> 2);
-    pdl_wait();
+    // `cur` serves upc consecutive units of a tile (4 / gpb k blocks), `nxt` the units after them
+    const int upc = max(1, 4 / (gpb * ks));
+    W4Walk at(p, u0), pre = at;
+    int pre_left = nu;                                  // units from `pre` to the end
+    auto fetch_pre = [&]() {
 #pragma unroll
-    for (int c = 0; c < NT; ++c) acc[c] = 0.f;
-    for (int i = 0; i < nu; ++i) {
-      const long long u = u0 + i;
-      const int kb = kblock(u);
-      const long long key = (u / p.kbu) << 32 | (uint32_t)(kb * gpb >> 2);
-      if (key != have) {
-        cur = nxt;
-        have = key;
-        // the next chunk that this thread needs: of this tile, or of the next tile's first unit
-        const int step = ks == 4 ? 1 : max(1, 4 / gpb - (kb & (4 / gpb - 1)));
-        const long long un = ks == 4 ? u + 1 : min(u + step, (u / p.kbu + 1) * p.kbu);
-        if (un < u1) nxt = fetch(nrow(un), kblock(un) * gpb >> 2);
+      for (int e = 0; e < 2; ++e) {
+        const int kb = pre.kb * ks + (2 * wg + e) % ks;
+        nxt[e] = fetch(pre.rowt * rpt + wrow + row, kb * gpb >> 2);
       }
-      const int g0 = (kb * gpb) & 3;                   // the block's first group in the chunk
+      do {                                              // to the first unit of the next chunk
+        pre.next(p);
+        --pre_left;
+      } while (pre.kb % upc != 0 && pre_left > 0);
+    };
+    fetch_pre();
+    pdl_wait();
+    auto clear = [&]() {
+#pragma unroll
+      for (int c = 0; c < NT; ++c) acc[c] = 0.f;
+    };
+    clear();
+    for (int i = 0; i < nu; ++i, at.next(p)) {
+      if (i == 0 || at.kb % upc == 0) {
+        cur[0] = nxt[0];
+        cur[1] = nxt[1];
+        if (pre_left > 0) fetch_pre();
+      }
       if (ok && !mbar_wait(&sh->full[st], ph)) ok = false;
       if (ok) {
-        const uint8_t* src = smem + st * stage + w * kWBox + row * 64;
-        const int sw = (row >> 1) & 3;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint4 q4 = *reinterpret_cast<const uint4*>(src + ((c ^ sw) << 4));
-          const uint32_t qw[4] = {q4.x, q4.y, q4.z, q4.w};
-          const int g = g0 + (c * gpb >> 2);
-          const uint32_t z = (cur.z >> (8 * g)) & 15u;
-          const uint32_t zz = 0x43004300u | z | z << 16;
-          uint32_t v[16];
+        for (int e = 0; e < 2; ++e) {
+          const int w = 2 * wg + e;
+          const int g0 = ((at.kb * ks + w % ks) * gpb) & 3;
+          const uint8_t* src = smem + st * stage + w * kWBox + row * 64;
+          const int sw = (row >> 1) & 3;
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+          for (int c = 0; c < 4; ++c) {
+            const uint4 q4 = *reinterpret_cast<const uint4*>(src + ((c ^ sw) << 4));
+            const uint32_t qw[4] = {q4.x, q4.y, q4.z, q4.w};
+            const uint32_t z = (cur[e].z >> (8 * (g0 + (c * gpb >> 2)))) & 15u;
+            const uint32_t zz = 0x43004300u | z | z << 16;
+            uint32_t v[16];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              v[4 * j + e] = sub_pair(((qw[j] >> (4 * e)) & 0x000f000fu) | 0x43004300u, zz);
-          tmem_st16_async(la + 16 * c, v);
-        }
-        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&sh->a_full[w]);
-          mbar_arrive(&sh->empty[st]);
-        }
-        for (int rd = 0; ok && rd < rounds; ++rd) {
-          if (!mbar_wait(&sh->d_full[w], dph)) { ok = false; break; }
-          dph ^= 1;
-          tc_fence_after();
-          for (int g = 0; g < per_round; ++g) {
-            const float s = scale_of(g0 + rd * per_round + g);
+            for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int c = 0; c < NT; c += 16) {
-              float d[16];
-              tmem_ld16(ld + NT * g + c, d);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) acc[c + e] += s * d[e];
-            }
+              for (int b = 0; b < 4; ++b)
+                v[4 * j + b] = sub_pair(((qw[j] >> (4 * b)) & 0x000f000fu) | 0x43004300u, zz);
+            tmem_st16_async(la + 64 * e + 16 * c, v);
           }
+          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
           tc_fence_before();
           __syncwarp();
-          if (rd + 1 < rounds && lane == 0) mbar_arrive(&sh->d_free[w]);
+          if (lane == 0) {
+            mbar_arrive(&sh->a_full[w]);
+            if (e == 1) mbar_arrive(&sh->empty[st]);
+          }
+        }
+        for (int rd = 0; ok && rd < rounds; ++rd) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int w = 2 * wg + e;
+            const int g0 = ((at.kb * ks + w % ks) * gpb) & 3;
+            if (ok && !mbar_wait(&sh->d_full[w], dph)) ok = false;
+            tc_fence_after();
+            for (int g = 0; g < per_round; ++g) {
+              const int gi = g0 + rd * per_round + g;
+              const uint32_t sv = (gi & 2) ? cur[e].s23 : cur[e].s01;
+              const float s = __uint_as_float((gi & 1) ? (sv & 0xffff0000u) : (sv << 16));
+#pragma unroll
+              for (int c = 0; c < NT; c += kLd) {
+                float d[kLd];
+                if constexpr (kLd == 32) tmem_ld32(ld + 64 * e + NT * g + c, d);
+                else tmem_ld16(ld + 64 * e + NT * g + c, d);
+#pragma unroll
+                for (int b = 0; b < kLd; b += 2)
+                  ffma2_acc(acc[c + b], acc[c + b + 1], d[b], d[b + 1], s);
+              }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (rd + 1 < rounds && lane == 0) mbar_arrive(&sh->d_free[w]);
+          }
+          dph ^= 1;
         }
       }
       if (++st == p.stages) { st = 0; ph ^= 1; }
 
       // ------------------------------------------------ the end of this CTA's part of a tile
-      const bool tile_end = (u + 1) % p.kbu == 0;
+      const bool tile_end = at.kb + 1 == p.kbu;
       if (!tile_end && i + 1 < nu) continue;
-      const int tile = (int)(u / p.kbu);
-      const int m0 = tile % p.chunks * NT, mv = min(NT, p.M - m0);
-      const int n = nrow(u);
-      if (ks == 4) {                                    // add the four k blocks' sums
-        for (int o = 1; o < 4; ++o) {
-          if (w == o) {
+      const int tile = at.tile;
+      const int m0 = at.chunk * NT, mv = min(NT, p.M - m0);
+      if constexpr (KS == 4) {                          // add the other warpgroup's sums
+        if (wg == 1) {
 #pragma unroll
-            for (int c = 0; c < NT; ++c) red[c * 128 + row] = acc[c];
-          }
-          w4_sync();
-          if (w == 0) {
+          for (int c = 0; c < NT; ++c) red[c * 128 + row] = acc[c];
+        }
+        w4_sync();
+        if (wg == 0) {
 #pragma unroll
-            for (int c = 0; c < NT; ++c) acc[c] += red[c * 128 + row];
-          }
-          w4_sync();
+          for (int c = 0; c < NT; ++c) acc[c] += red[c * 128 + row];
         }
       }
-      const bool mine = ks == 1 || w == 0;
-      const long long t0 = (long long)tile * p.kbu, t1 = t0 + p.kbu;
+      const bool mine = ks == 2 || wg == 0;
+      const int t0 = u0 + i - at.kb, t1 = t0 + p.kbu;
       auto put = [&](int m, int nn, float v) {
         if (p.bias) v += __uint_as_float((uint32_t)__ldg(p.bias + nn) << 16);
-        const int64_t at = (int64_t)(m0 + m) * p.out_stride + nn;
-        if (p.out_f32) reinterpret_cast<float*>(p.out)[at] = v;
-        else reinterpret_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
+        const int64_t o = (int64_t)(m0 + m) * p.out_stride + nn;
+        if (p.out_f32) reinterpret_cast<float*>(p.out)[o] = v;
+        else reinterpret_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(v);
       };
       if (u0 <= t0 && tile_end) {                       // the whole tile
+        const int n = at.rowt * rpt + wrow + row;
         if (mine && n < p.N) {
 #pragma unroll
           for (int c = 0; c < NT; ++c)
@@ -372,7 +415,7 @@ w4_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
           return p.part + ((int64_t)2 * c + (first ? 0 : 1)) * NT * rpt;
         };
         if (mine) {
-          float* dst = slot(blockIdx.x) + (ks == 1 ? w * 128 : 0) + row;
+          float* dst = slot(blockIdx.x) + wrow + row;
 #pragma unroll
           for (int c = 0; c < NT; ++c)
             if (c < mv) dst[c * rpt] = acc[c];
@@ -383,17 +426,16 @@ w4_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
         w4_sync();
         if (sh->last) {
           __threadfence();
-          const int rr = (threadIdx.x - 128) & (rpt - 1);
-          const int nn = tile / p.chunks * rpt + rr;
-          for (int m = (threadIdx.x - 128) / rpt; m < mv; m += 512 / rpt) {
+          for (int o = threadIdx.x - 128; o < mv * rpt; o += 256) {
+            const int rr = o & (rpt - 1), nn = at.rowt * rpt + rr;
             float v = 0.f;
-            for (int c = c0; c <= c1; ++c) v += __ldcg(slot(c) + m * rpt + rr);
-            if (nn < p.N) put(m, nn, v);
+            for (int c = c0; c <= c1; ++c) v += __ldcg(slot(c) + o);
+            if (nn < p.N) put(o / rpt, nn, v);
           }
         }
       }
-#pragma unroll
-      for (int c = 0; c < NT; ++c) acc[c] = 0.f;
+      if constexpr (KS == 4) w4_sync();                 // `red` is free again
+      clear();
     }
     if (!ok && lane == 0) report(p.ws, ETREE_ETIMEOUT, DET_WAIT_W4);
   }
@@ -424,9 +466,9 @@ cudaError_t launch_w4(const CUtensorMap& q, const CUtensorMap& x, W4Params p, in
     if (e != cudaSuccess) return e;
     return launch_pdl(kernel, dim3(grid), dim3(kWThreads), (size_t)kWSmem, s, q, x, p);
   };
-  if (nt == 16) return go(w4_kernel<16>);
-  if (nt == 32) return go(w4_kernel<32>);
-  return go(w4_kernel<64>);
+  if (p.ks == 4)
+    return nt == 16 ? go(w4_kernel<16, 4>) : nt == 32 ? go(w4_kernel<32, 4>) : go(w4_kernel<64, 4>);
+  return nt == 16 ? go(w4_kernel<16, 2>) : nt == 32 ? go(w4_kernel<32, 2>) : go(w4_kernel<64, 2>);
 }
 
 }  // namespace etree
