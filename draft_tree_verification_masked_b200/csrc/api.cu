@@ -868,7 +868,7 @@ static W4Plan plan_w4(int M, int N, int K) {          // checked arguments: unit
   pl.nt = M <= 16 ? 16 : M <= 32 ? 32 : 64;
   pl.chunks = (M + pl.nt - 1) / pl.nt;
   const int nkb = (K + 127) / 128;
-  pl.ks = (int64_t)((N + 255) / 256) * pl.chunks >= sms ? 2 : 4;
+  pl.ks = pl.nt == 64 || (int64_t)((N + 255) / 256) * pl.chunks >= sms ? 2 : 4;
   const int rpt = pl.ks == 4 ? 128 : 256;
   pl.kbu = (nkb + pl.ks - 1) / pl.ks;
   pl.tiles = (N + rpt - 1) / rpt * pl.chunks;

@@ -229,7 +229,6 @@ struct W4Params {
   int M, N, K, group, out_f32, units;
   int ks, kbu, chunks, tiles, stages;   // k blocks a unit; units a tile; token chunks; tiles
 };
-int w4_stages(int nt, int ks);
 cudaError_t launch_w4(const CUtensorMap& q, const CUtensorMap& x, W4Params p, int nt, int grid,
                       cudaStream_t s);
 
