@@ -81,6 +81,14 @@ __device__ __forceinline__ void tmem_st16_async(uint32_t taddr, const uint32_t (
       : "memory");
 }
 
+// The bf16 pair (128 + q, 128 + q') of the nibbles at bits 0 and 16: (w & 0x000f000f) | magic in one
+// operation, with the second constant in a register.
+__device__ __forceinline__ uint32_t nibble_pair(uint32_t w, uint32_t magic) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xEA;" : "=r"(r) : "r"(w), "r"(magic));
+  return r;
+}
+
 // a - b on bf16 pairs (exact here: integers of magnitude below 256).
 __device__ __forceinline__ uint32_t sub_pair(uint32_t a, uint32_t b) {
   const __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&a),
@@ -153,25 +161,27 @@ __device__ __noinline__ void w4_unpack(const W4Params& p, const W4Cta& c, int nu
   struct Groups {
     uint32_t s01, s23, z;
   };
+  // The loads are unconditional, at addresses kept inside the arrays, so that nothing waits for
+  // them before they are used; rows and groups behind the end get the scale 0 there.
   auto fetch = [&](const W4Walk& at, int e) -> Groups {
-    Groups r{0u, 0u, 0x08080808u};
-    const int n = at.rowt * rpt + wrow;
+    const int n = min(at.rowt * rpt + wrow, p.N - 1);
     const int g = ((at.kb * ks + (2 * wg + e) % ks) * gpb) & ~3;
-    if (n >= p.N || g >= ng) return r;
-    const int64_t o = (int64_t)n * ng + g;
+    const int64_t o = (int64_t)n * ng + min(g, ng - (wide ? 4 : 1));
+    Groups r;
+    r.z = 0x08080808u;
     if (wide) {
       const uint2 s = __ldg(reinterpret_cast<const uint2*>(p.scales + o));
       r.s01 = s.x;
       r.s23 = s.y;
       if (p.zeros) r.z = __ldg(reinterpret_cast<const uint32_t*>(p.zeros + o));
     } else {
-      uint32_t s[4] = {0u, 0u, 0u, 0u}, z[4] = {8u, 8u, 8u, 8u};
+      uint32_t s[4], z[4] = {8u, 8u, 8u, 8u};
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (g + j < ng) {
-          s[j] = __ldg(p.scales + o + j);
-          if (p.zeros) z[j] = __ldg(p.zeros + o + j);
-        }
+      for (int j = 0; j < 4; ++j) {
+        const int64_t oj = (int64_t)n * ng + min(g + j, ng - 1);
+        s[j] = __ldg(p.scales + oj);
+        if (p.zeros) z[j] = __ldg(p.zeros + oj);
+      }
       r.s01 = s[0] | s[1] << 16;
       r.s23 = s[2] | s[3] << 16;
       r.z = z[0] | z[1] << 8 | z[2] << 16 | z[3] << 24;
@@ -190,6 +200,8 @@ __device__ __noinline__ void w4_unpack(const W4Params& p, const W4Cta& c, int nu
     } while ((pre.kb & (upc - 1)) != 0 && pre_left > 0);
   };
   fetch_pre();
+  uint32_t magic = 0x43004300u;
+  asm volatile("" : "+r"(magic));                        // stays in a register
   bool ok = true;
   int st = 0;
   uint32_t ph = 0;
@@ -219,9 +231,13 @@ __device__ __noinline__ void w4_unpack(const W4Params& p, const W4Cta& c, int nu
       if (i > 0 && !mbar_wait(&sh->a_free[w], (i - 1) & 1)) { ok = false; break; }
       tc_fence_after();
       float* sc = scale_s + ((i & 1) * 4 + w) * gpb * 128 + row;
+      const int gb = (at.kb * ks + w % ks) * gpb;       // the block's first group
+      const bool in = at.rowt * rpt + wrow < p.N;
       for (int g = 0; g < gpb; ++g) {
         const uint32_t sv = ((g0 + g) & 2) ? cur[e].s23 : cur[e].s01;
-        sc[g * 128] = __uint_as_float(((g0 + g) & 1) ? (sv & 0xffff0000u) : (sv << 16));
+        sc[g * 128] = in && gb + g < ng
+                          ? __uint_as_float(((g0 + g) & 1) ? (sv & 0xffff0000u) : (sv << 16))
+                          : 0.f;
       }
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
@@ -232,7 +248,7 @@ __device__ __noinline__ void w4_unpack(const W4Params& p, const W4Cta& c, int nu
         for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int b = 0; b < 4; ++b)
-            v[4 * j + b] = sub_pair(((qw[4 * c + j] >> (4 * b)) & 0x000f000fu) | 0x43004300u, zz);
+            v[4 * j + b] = sub_pair(nibble_pair(qw[4 * c + j] >> (4 * b), magic), zz);
         tmem_st16_async(la + 64 * e + 16 * c, v);
       }
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
