@@ -855,8 +855,7 @@ etree_status etree_verify_attn_diff_paged(
 
 // ------------------------------------------------------------------ products with 4-bit weights
 struct W4Plan {
-  int nt, ks, chunks, kbu, tiles, grid;
-  int64_t units;
+  int nt, ks, chunks, kbu, tiles, grid, whole, share_units, share_grid;
   size_t count, xp, part, total;
 };
 
@@ -872,8 +871,10 @@ static W4Plan plan_w4(int M, int N, int K) {          // checked arguments: unit
   const int rpt = pl.ks == 4 ? 128 : 256;
   pl.kbu = (nkb + pl.ks - 1) / pl.ks;
   pl.tiles = (N + rpt - 1) / rpt * pl.chunks;
-  pl.units = (int64_t)pl.tiles * pl.kbu;
-  pl.grid = (int)std::min<int64_t>(pl.units, sms);
+  pl.grid = (int)std::min<int64_t>((int64_t)pl.tiles * pl.kbu, sms);
+  pl.whole = pl.tiles / pl.grid;                       // the tiles left over are shared by units
+  pl.share_units = (pl.tiles - pl.whole * pl.grid) * pl.kbu;
+  pl.share_grid = std::min(pl.share_units, pl.grid);
   pl.count = up256(sizeof(WsHeader));
   pl.xp = up256(pl.count + (size_t)pl.tiles * sizeof(int32_t));
   pl.part = up256(pl.xp + (size_t)pl.chunks * pl.nt * K * 2);
@@ -943,12 +944,13 @@ etree_status etree_w4_linear(const uint16_t* x, int64_t x_stride, int M, const u
   p.N = N;
   p.K = K;
   p.group = group;
-  p.ks = pl.ks;
   p.kbu = pl.kbu;
   p.chunks = pl.chunks;
   p.tiles = pl.tiles;
-  p.units = (int)pl.units;
-  cudaError_t e = launch_w4(tq, tx, p, pl.nt, pl.grid, static_cast<cudaStream_t>(stream));
+  p.whole = pl.whole;
+  p.share_units = pl.share_units;
+  p.share_grid = pl.share_grid;
+  cudaError_t e = launch_w4(tq, tx, p, pl.nt, pl.ks, pl.grid, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ETREE_OK : cuda_fail(e, "etree_w4_linear launch");
 }
 

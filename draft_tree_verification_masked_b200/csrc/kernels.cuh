@@ -226,10 +226,11 @@ struct W4Params {
   int32_t* count;                   // workspace: per tile, the CTAs that delivered their part
   WsHeader* ws;
   int64_t x_stride, out_stride;
-  int M, N, K, group, out_f32, units;
-  int ks, kbu, chunks, tiles, stages;   // k blocks a unit; units a tile; token chunks; tiles
+  int M, N, K, group, out_f32;
+  int kbu, chunks, tiles;           // units a tile, token chunks, tiles
+  int whole, share_units, share_grid;   // whole tiles a CTA; the other tiles' units, and their CTAs
 };
-cudaError_t launch_w4(const CUtensorMap& q, const CUtensorMap& x, W4Params p, int nt, int grid,
-                      cudaStream_t s);
+cudaError_t launch_w4(const CUtensorMap& q, const CUtensorMap& x, const W4Params& p, int nt, int ks,
+                      int grid, cudaStream_t s);
 
 }  // namespace etree

@@ -31,21 +31,41 @@
 namespace etree {
 
 namespace {
-constexpr int kWThreads = 32 * 20;          // TMA, two MMA, one idle, 8 unpacking, 8 summing warps
+constexpr int kWThreads = 32 * 20;          // TMA, two MMA, one scale, 8 unpacking, 8 summing warps
 constexpr int kWBox = 128 * 64;             // [128 rows][64 bytes]
 constexpr int kWMaxStages = 5;
 constexpr int kWSmem = 226 * 1024;
 
 struct W4Smem {
   uint64_t full[kWMaxStages], empty[kWMaxStages];
-  uint64_t a_full[4], a_free[4], d_full[4], d_free[4], s_full[4][2], drain[2];
+  uint64_t a_full[4], a_free[4], d_full[4], d_free[4], drain[2];
   uint32_t tmem;
   int last;
 };
 
+// NT tokens a tile, KS k blocks a unit (of 4 / KS row tiles), GPB groups a k block of 128.
+template <int NT, int KS, int GPB>
+struct W4Shape {
+  static constexpr int kRows = 512 / KS;                // rows of a tile
+  static constexpr int kX = NT * 256;                   // one k block of x: two boxes [NT][64]
+  // scales and zero points of a unit: a warpgroup's 2 GPB groups of its 128 rows, as 32-bit words
+  // [word][256]
+  static constexpr int kSWords = GPB, kZWords = (2 * GPB + 3) / 4;
+  static constexpr int kTx = 4 * kWBox + KS * kX;       // bytes that TMA brings
+  static constexpr int kStage = kTx + (kSWords + kZWords) * 1024;
+  static constexpr int kRed = KS == 4 ? NT * 512 : 0;   // one warpgroup's sums
+  static constexpr int kFixed = 1024 + kRed + (int)sizeof(W4Smem);
+  static constexpr int kFit = (kWSmem - kFixed) / kStage;
+  static constexpr int kStages = kFit < kWMaxStages ? kFit : kWMaxStages;
+  static constexpr int kPerRound = GPB < 64 / NT ? GPB : 64 / NT;   // groups that D holds at once
+  static constexpr int kRounds = GPB / kPerRound;
+  static_assert(kStages >= 2, "two stages at least");
+};
+
 __device__ __forceinline__ void w4_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
-// First unit of CTA c, and the CTA that holds unit u.
+// The units of the shared tiles are dealt to the first `grid` CTAs: CTA c's first one, and the CTA
+// that holds unit u.
 __device__ __forceinline__ int w4_first(int units, int grid, int c) {
   return (int)((int64_t)units * c / grid);
 }
@@ -53,24 +73,52 @@ __device__ __forceinline__ int w4_owner(int units, int grid, int u) {
   return (int)(((int64_t)(u + 1) * grid - 1) / units);
 }
 
-// A CTA's walk over its units: the tile, its row and token chunk, and the unit's place in depth.
-struct W4Walk {
-  int tile, kb, rowt, chunk;
-  __device__ __forceinline__ W4Walk(const W4Params& p, int u) {
-    tile = u / p.kbu;
-    kb = u - tile * p.kbu;
-    rowt = tile / p.chunks;
-    chunk = tile - rowt * p.chunks;
-  }
-  __device__ __forceinline__ void next(const W4Params& p) {
-    if (++kb < p.kbu) return;
-    kb = 0;
-    ++tile;
-    if (++chunk < p.chunks) return;
-    chunk = 0;
-    ++rowt;
-  }
+// A CTA's segments in order: its share of the shared tiles' units, at most the end of one tile and
+// the start of the next, then `whole` tiles of its own.  Every role walks the same list.
+struct W4Segment {
+  int rowt, chunk, tile, kb, n, unit0;                  // n units from kb; unit0: the shared unit
+  bool part;
 };
+__device__ __forceinline__ bool w4_segment(const W4Params& p, int s, W4Segment& at) {
+  if ((int)blockIdx.x < p.share_grid) {
+    int u = w4_first(p.share_units, p.share_grid, blockIdx.x);
+    const int end = w4_first(p.share_units, p.share_grid, blockIdx.x + 1);
+    int t = u / p.kbu;
+    const int split = min(end, (t + 1) * p.kbu);
+    if (s == 1 && split < end) {
+      u = split;
+      ++t;
+    }
+    if (s == 0 || (s == 1 && split < end)) {
+      at.kb = u - t * p.kbu;
+      at.n = (u < split ? split : end) - u;
+      at.tile = p.tiles - p.share_units / p.kbu + t;
+      at.unit0 = u;
+      at.part = at.n < p.kbu;
+      at.rowt = at.tile / p.chunks;
+      at.chunk = at.tile - at.rowt * p.chunks;
+      return true;
+    }
+    s -= split < end ? 2 : 1;
+  }
+  if (s >= p.whole) return false;
+  at.kb = 0;
+  at.n = p.kbu;
+  at.tile = blockIdx.x * p.whole + s;
+  at.unit0 = 0;
+  at.part = false;
+  at.rowt = at.tile / p.chunks;
+  at.chunk = at.tile - at.rowt * p.chunks;
+  return true;
+}
+
+// The units of this CTA.
+__device__ __forceinline__ int units_of(const W4Params& p) {
+  const int own = p.whole * p.kbu;
+  if ((int)blockIdx.x >= p.share_grid) return own;
+  return own + w4_first(p.share_units, p.share_grid, blockIdx.x + 1) -
+         w4_first(p.share_units, p.share_grid, blockIdx.x);
+}
 
 __device__ __forceinline__ void tmem_st16_async(uint32_t taddr, const uint32_t (&v)[16]) {
   asm volatile(
@@ -106,6 +154,40 @@ __device__ __forceinline__ void ffma2_acc(uint64_t& acc, float v0, float v1, flo
 __device__ __forceinline__ float half_of(uint64_t acc, int i) {
   return __uint_as_float((uint32_t)(acc >> (32 * i)));
 }
+
+// CNT consecutive elements of a row of ng scales (or zero points) from index g, packed into 32-bit
+// words.  The addresses stay inside the row, so that the loads need no condition; the caller
+// drops what lies behind the row's end.
+template <int CNT, typename T>
+struct W4Row {
+  static constexpr int kBytes = CNT * (int)sizeof(T), kWords = (kBytes + 3) / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void fetch(const T* row, int g, int ng, bool wide) {
+    if (wide) {                                         // ng is a multiple of CNT
+      const T* at = row + min(g, ng - CNT);
+      if constexpr (kBytes == 2) w[0] = __ldg(reinterpret_cast<const uint16_t*>(at));
+      else if constexpr (kBytes == 4) w[0] = __ldg(reinterpret_cast<const uint32_t*>(at));
+      else if constexpr (kBytes == 8) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(at));
+        w[0] = v.x;
+        w[1] = v.y;
+      } else {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(at));
+        w[0] = v.x;
+        w[1] = v.y;
+        w[2] = v.z;
+        w[3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) w[i] = 0u;
+#pragma unroll
+      for (int i = 0; i < CNT; ++i)
+        w[i * sizeof(T) / 4] |= (uint32_t)__ldg(row + min(g + i, ng - 1))
+                                << (8 * sizeof(T) * (i % (4 / sizeof(T))));
+    }
+  }
+};
 }  // namespace
 
 // x [M][K] (rows x_stride apart) -> xp [rows][K], every eight values as 0 4 1 5 2 6 3 7 and rows
@@ -128,121 +210,104 @@ __global__ void __launch_bounds__(256) w4_prepare_kernel(W4Params p, int rows) {
   reinterpret_cast<uint4*>(p.xp)[i] = v;
 }
 
-// What the roles share: pieces of shared memory, the first unit and the TMEM base.
-struct W4Cta {
-  uint8_t* smem;
-  float *red, *scale_s;
-  W4Smem* sh;
-  int u0;
-  uint32_t tmem;
-};
+// One warp brings the scales and zero points, a few bytes of each row: eight rows a lane, the next
+// unit's loads in flight while this one's stage is awaited.
+template <int NT, int KS, int GPB>
+__device__ __noinline__ void w4_scales(const W4Params& p, uint8_t* smem, W4Smem* sh) {
+  using Sh = W4Shape<NT, KS, GPB>;
+  const int lane = threadIdx.x & 31, ng = p.K / p.group;
+  const bool wide = ng % (2 * GPB) == 0;
+  W4Row<2 * GPB, uint16_t> sc[8];
+  W4Row<2 * GPB, uint8_t> zp[8];
+#pragma unroll
+  for (int r = 0; r < 8; ++r)
+#pragma unroll
+    for (int j = 0; j < Sh::kZWords; ++j) zp[r].w[j] = 0x08080808u;
+  auto fetch = [&](int rowt, int kb) {
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const int i = r * 32 + lane, wg = i >> 7;         // row i of the unit's 2 x 128
+      const int n = min(rowt * Sh::kRows + (KS == 4 ? i & 127 : i), p.N - 1);
+      const int g = (kb * KS + (KS == 4 ? 2 * wg : 0)) * GPB;
+      sc[r].fetch(p.scales + (int64_t)n * ng, g, ng, wide);
+      if (p.zeros) zp[r].fetch(p.zeros + (int64_t)n * ng, g, ng, wide);
+    }
+  };
+  W4Segment at;
+  int seg = 0;
+  bool more = w4_segment(p, seg, at);
+  int kb = at.kb, left = at.n, st = 0;
+  uint32_t ph = 1;                                      // the first round of stages is free
+  bool ok = true;
+  if (more) fetch(at.rowt, kb);
+  while (more) {
+    if (!mbar_wait(&sh->empty[st], ph)) { ok = false; break; }
+    uint32_t* dst = reinterpret_cast<uint32_t*>(smem + st * Sh::kStage + Sh::kTx) + lane;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+#pragma unroll
+      for (int j = 0; j < Sh::kSWords; ++j) dst[j * 256 + r * 32] = sc[r].w[j];
+#pragma unroll
+      for (int j = 0; j < Sh::kZWords; ++j) dst[(Sh::kSWords + j) * 256 + r * 32] = zp[r].w[j];
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh->full[st]);
+    if (++st == Sh::kStages) { st = 0; ph ^= 1; }
+    ++kb;
+    if (--left == 0) {                                  // the next unit is another segment's
+      more = w4_segment(p, ++seg, at);
+      kb = at.kb;
+      left = at.n;
+    }
+    if (more) fetch(at.rowt, kb);
+  }
+  if (!ok && lane == 0) report(p.ws, ETREE_ETIMEOUT, DET_WAIT_W4);
+}
 
 // The two roles with many live registers are functions of their own, so that each is allocated
 // apart (inlined side by side they spilled in the inner loops).
-template <int NT, int KS>
-__device__ __noinline__ void w4_unpack(const W4Params& p, const W4Cta& c, int nu) {
+//
+// Unpacking: warpgroup wg turns blocks 2 wg and 2 wg + 1 of every unit into A in TMEM.
+template <int NT, int KS, int GPB>
+__device__ __noinline__ void w4_unpack(const W4Params& p, uint8_t* smem, W4Smem* sh, uint32_t tmem,
+                                       int nu) {
+  using Sh = W4Shape<NT, KS, GPB>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int ks = KS, rpt = KS == 4 ? 128 : 256;
-  W4Smem* const sh = c.sh;
-  float* const scale_s = c.scale_s;
-  const int u0 = c.u0, gpb = 128 / p.group, ng = p.K / p.group;
-  const uint32_t tmem = c.tmem;
-  uint8_t* const smem = c.smem;
-  constexpr int stage = 4 * kWBox + ks * NT * 256;
-  const bool wide = (ng & 3) == 0;                      // four groups of a row in one load
-  const int upc = max(1, 4 / (gpb * ks));               // units that four groups serve
-  // ------------------------------------------------------------------------- q to A in TMEM
   const int wg = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
-  const int wrow = (ks == 4 ? 0 : wg * 128) + row;    // the row in the tile
   const uint32_t la = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 128 * wg;
   const int sw = (row >> 1) & 3;
-  // scales and zero points of four consecutive groups: `cur` serves upc units of a tile, `nxt`
-  // the units after them
-  struct Groups {
-    uint32_t s01, s23, z;
-  };
-  // The loads are unconditional, at addresses kept inside the arrays, so that nothing waits for
-  // them before they are used; rows and groups behind the end get the scale 0 there.
-  auto fetch = [&](const W4Walk& at, int e) -> Groups {
-    const int n = min(at.rowt * rpt + wrow, p.N - 1);
-    const int g = ((at.kb * ks + (2 * wg + e) % ks) * gpb) & ~3;
-    const int64_t o = (int64_t)n * ng + min(g, ng - (wide ? 4 : 1));
-    Groups r;
-    r.z = 0x08080808u;
-    if (wide) {
-      const uint2 s = __ldg(reinterpret_cast<const uint2*>(p.scales + o));
-      r.s01 = s.x;
-      r.s23 = s.y;
-      if (p.zeros) r.z = __ldg(reinterpret_cast<const uint32_t*>(p.zeros + o));
-    } else {
-      uint32_t s[4], z[4] = {8u, 8u, 8u, 8u};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int64_t oj = (int64_t)n * ng + min(g + j, ng - 1);
-        s[j] = __ldg(p.scales + oj);
-        if (p.zeros) z[j] = __ldg(p.zeros + oj);
-      }
-      r.s01 = s[0] | s[1] << 16;
-      r.s23 = s[2] | s[3] << 16;
-      r.z = z[0] | z[1] << 8 | z[2] << 16 | z[3] << 24;
-    }
-    return r;
-  };
-  Groups cur[2], nxt[2];
-  W4Walk at(p, u0), pre = at;
-  int pre_left = nu;                                  // units from `pre` to the end
-  auto fetch_pre = [&]() {
-    nxt[0] = fetch(pre, 0);
-    nxt[1] = fetch(pre, 1);
-    do {                                              // to the first unit of the next chunk
-      pre.next(p);
-      --pre_left;
-    } while ((pre.kb & (upc - 1)) != 0 && pre_left > 0);
-  };
-  fetch_pre();
   uint32_t magic = 0x43004300u;
-  asm volatile("" : "+r"(magic));                        // stays in a register
-  bool ok = true;
+  asm volatile("" : "+r"(magic));                       // stays in a register
   int st = 0;
-  uint32_t ph = 0;
-  for (int i = 0; ok && i < nu; ++i, at.next(p)) {
-    if (i == 0 || (at.kb & (upc - 1)) == 0) {
-      cur[0] = nxt[0];
-      cur[1] = nxt[1];
-      if (pre_left > 0) fetch_pre();
-    }
+  uint32_t ph = 0, done = 0;                            // units done, modulo 2 (as parity)
+  const uint8_t* src0 = smem + 2 * wg * kWBox + row * 64;
+  const uint8_t* src = src0;
+  const uint8_t* zp0 = smem + Sh::kTx + Sh::kSWords * 1024 + (wg * 128 + row) * 4;
+  bool ok = true;
+  for (int i = 0; i < nu; ++i) {
     if (!mbar_wait(&sh->full[st], ph)) { ok = false; break; }
+    uint32_t zw[Sh::kZWords];
+#pragma unroll
+    for (int j = 0; j < Sh::kZWords; ++j)
+      zw[j] = *reinterpret_cast<const uint32_t*>(zp0 + st * Sh::kStage + j * 1024);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int w = 2 * wg + e;
-      const int g0 = ((at.kb * ks + w % ks) * gpb) & 3;
-      const uint8_t* src = smem + st * stage + w * kWBox + row * 64;
       uint32_t qw[16];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const uint4 q = *reinterpret_cast<const uint4*>(src + ((c ^ sw) << 4));
+        const uint4 q = *reinterpret_cast<const uint4*>(src + e * kWBox + ((c ^ sw) << 4));
         qw[4 * c] = q.x;
         qw[4 * c + 1] = q.y;
         qw[4 * c + 2] = q.z;
         qw[4 * c + 3] = q.w;
       }
-      // A is free again; this also says that the summing warps are done with unit i - 2, whose
-      // scales lie where unit i's go
-      if (i > 0 && !mbar_wait(&sh->a_free[w], (i - 1) & 1)) { ok = false; break; }
+      if (i > 0 && !mbar_wait(&sh->a_free[2 * wg + e], done ^ 1)) { ok = false; break; }
       tc_fence_after();
-      float* sc = scale_s + ((i & 1) * 4 + w) * gpb * 128 + row;
-      const int gb = (at.kb * ks + w % ks) * gpb;       // the block's first group
-      const bool in = at.rowt * rpt + wrow < p.N;
-      for (int g = 0; g < gpb; ++g) {
-        const uint32_t sv = ((g0 + g) & 2) ? cur[e].s23 : cur[e].s01;
-        sc[g * 128] = in && gb + g < ng
-                          ? __uint_as_float(((g0 + g) & 1) ? (sv & 0xffff0000u) : (sv << 16))
-                          : 0.f;
-      }
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const uint32_t z = (cur[e].z >> (8 * (g0 + (c * gpb >> 2)))) & 15u;
-        const uint32_t zz = 0x43004300u | z | z << 16;
+        const int zi = e * GPB + c * GPB / 4;           // this group's byte
+        const uint32_t z = (zw[zi / 4] >> (8 * (zi % 4))) & 15u;
+        const uint32_t zz = z * 0x00010001u | magic;
         uint32_t v[16];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -254,73 +319,87 @@ __device__ __noinline__ void w4_unpack(const W4Params& p, const W4Cta& c, int nu
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&sh->s_full[w][i & 1]);
-        mbar_arrive(&sh->a_full[w]);
-        if (e == 1) mbar_arrive(&sh->empty[st]);
-      }
+      if (lane == 0) mbar_arrive(&sh->a_full[2 * wg + e]);
     }
-    if (++st == p.stages) { st = 0; ph ^= 1; }
+    if (!ok) break;
+    if (lane == 0) mbar_arrive(&sh->empty[st]);
+    done ^= 1;
+    src += Sh::kStage;
+    if (++st == Sh::kStages) {
+      st = 0;
+      ph ^= 1;
+      src = src0;
+    }
   }
   if (!ok && lane == 0) report(p.ws, ETREE_ETIMEOUT, DET_WAIT_W4);
 }
 
-template <int NT, int KS>
-__device__ __noinline__ void w4_sum(const W4Params& p, const W4Cta& c, int nu) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int ks = KS, rpt = KS == 4 ? 128 : 256;
-  W4Smem* const sh = c.sh;
-  float* const scale_s = c.scale_s;
-  const int u0 = c.u0, gpb = 128 / p.group;
-  const uint32_t tmem = c.tmem;
-  float* const red = c.red;
-  const int per_round = NT == 64 ? 1 : min(gpb, 64 / NT), rounds = gpb / per_round;
-  // ------------------------------------------------------- the scaled sums of the groups
-  const int wg = (warp - 12) >> 2, row = (warp & 3) * 32 + lane, tid = threadIdx.x - 12 * 32;
-  const int wrow = (ks == 4 ? 0 : wg * 128) + row;
+// Summing: warpgroup wg adds the scaled group sums of blocks 2 wg and 2 wg + 1, and writes the tile.
+template <int NT, int KS, int GPB>
+__device__ __noinline__ void w4_sum(const W4Params& p, const uint8_t* smem, float* red, W4Smem* sh,
+                                    uint32_t tmem) {
+  using Sh = W4Shape<NT, KS, GPB>;
+  constexpr int kRows = Sh::kRows;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x - 12 * 32;
+  const int wg = (warp - 12) >> 2, row = (warp & 3) * 32 + lane;
+  const int wrow = (KS == 4 ? 0 : wg * 128) + row;
   const uint32_t ld = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256 + 128 * wg;
+  const int ng = p.K / p.group;
+  const uint8_t* sp0 = smem + Sh::kTx + (wg * 128 + row) * 4;
   pdl_wait();
-  W4Walk at(p, u0);
-  uint64_t acc[NT / 2];                               // tokens 2 c and 2 c + 1
-  auto clear = [&]() {
+  uint64_t acc[NT / 2];                                 // tokens 2 c and 2 c + 1
+  uint32_t use = 0, ph = 0;
+  int st = 0;
+  bool ok = true;
+  W4Segment at;
+  for (int seg = 0; w4_segment(p, seg, at); ++seg) {
 #pragma unroll
     for (int c = 0; c < NT / 2; ++c) acc[c] = 0ull;
-  };
-  clear();
-  bool ok = true;
-  uint32_t use = 0;
-  for (int i = 0; i < nu; ++i, at.next(p)) {
-    for (int rd = 0; ok && rd < rounds; ++rd, ++use) {
+    for (int i = 0; i < at.n; ++i) {
+      const int g0 = ((at.kb + i) * KS + (KS == 4 ? 2 * wg : 0)) * GPB;
+      if (ok && !mbar_wait(&sh->full[st], ph)) ok = false;
+      uint32_t sc[Sh::kSWords];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int w = 2 * wg + e;
-        const float* sc = scale_s + (((i & 1) * 4 + w) * gpb + rd * per_round) * 128 + row;
-        if (ok && !mbar_wait(&sh->s_full[w][i & 1], (i >> 1) & 1)) ok = false;
-        if (ok && !mbar_wait(&sh->d_full[w], use & 1)) ok = false;
-        tc_fence_after();
-        for (int g = 0; g < per_round; ++g) {
-          const float s = sc[g * 128];
+      for (int j = 0; j < Sh::kSWords; ++j)
+        sc[j] = *reinterpret_cast<const uint32_t*>(sp0 + st * Sh::kStage + j * 1024);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->empty[st]);
+      if (++st == Sh::kStages) { st = 0; ph ^= 1; }
 #pragma unroll
-          for (int c = 0; c < NT; c += 16) {
-            float d[16];
-            tmem_ld16(ld + 64 * e + NT * g + c, d);
+      for (int rd = 0; rd < Sh::kRounds; ++rd) {
 #pragma unroll
-            for (int b = 0; b < 16; b += 2)
-              ffma2_acc(acc[(c + b) / 2], d[b], d[b + 1], s);
+        for (int e = 0; e < 2; ++e) {
+          if (ok && !mbar_wait(&sh->d_full[2 * wg + e], (use + rd) & 1)) ok = false;
+          tc_fence_after();
+#pragma unroll
+          for (int g = 0; g < Sh::kPerRound; ++g) {
+            const int si = e * GPB + rd * Sh::kPerRound + g;
+            if (g0 + si >= ng) continue;                // behind the row's end
+            const uint32_t sv = sc[si / 2];
+            const float s = __uint_as_float((si & 1) ? (sv & 0xffff0000u) : (sv << 16));
+#pragma unroll
+            for (int c = 0; c < NT; c += 16) {
+              float d[16];
+              tmem_ld16(ld + 64 * e + NT * g + c, d);
+#pragma unroll
+              for (int b = 0; b < 16; b += 2) ffma2_acc(acc[(c + b) / 2], d[b], d[b + 1], s);
+            }
           }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh->d_free[2 * wg + e]);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->d_free[w]);
       }
+      use += Sh::kRounds;
     }
 
-    // ------------------------------------------------ the end of this CTA's part of a tile
-    const bool tile_end = at.kb + 1 == p.kbu;
-    if (!tile_end && i + 1 < nu) continue;
-    const int tile = at.tile;
+    // ---------------------------------------------------------------- the segment's end
+    int again = seg;                                    // the segment anew: it was not kept in
+    asm volatile("" : "+r"(again));                     // registers beside the sums
+    w4_segment(p, again, at);
+    const int rowt = at.rowt, tile = at.tile;
     const int m0 = at.chunk * NT, mv = min(NT, p.M - m0);
-    if constexpr (KS == 4) {                          // add the other warpgroup's sums
+    if constexpr (KS == 4) {                            // add the other warpgroup's sums
       if (wg == 1) {
 #pragma unroll
         for (int c = 0; c < NT; ++c) red[c * 128 + row] = half_of(acc[c / 2], c & 1);
@@ -332,58 +411,67 @@ __device__ __noinline__ void w4_sum(const W4Params& p, const W4Cta& c, int nu) {
           ffma2_acc(acc[c / 2], red[c * 128 + row], red[(c + 1) * 128 + row], 1.f);
       }
     }
-    const bool mine = ks == 2 || wg == 0;
-    const int t0 = u0 + i - at.kb, t1 = t0 + p.kbu;
+    const bool mine = KS == 2 || wg == 0;
     auto bias_of = [&](int n) {
       return p.bias ? __uint_as_float((uint32_t)__ldg(p.bias + n) << 16) : 0.f;
     };
-    if (u0 <= t0 && tile_end) {                       // the whole tile
-      const int n = at.rowt * rpt + wrow;
+    if (!at.part) {
+      const int n = rowt * kRows + wrow;
       if (mine && n < p.N) {
         const float b = bias_of(n);
-        // one running pointer: 64 row offsets at once would push the sums out of the registers
+        // one running pointer: NT row offsets at once would push the sums out of the registers
         const int64_t step = p.out_stride * (p.out_f32 ? 4 : 2);
         char* dst = reinterpret_cast<char*>(p.out) +
                     ((int64_t)m0 * p.out_stride + n) * (p.out_f32 ? 4 : 2);
+        if (p.out_f32) {
 #pragma unroll
-        for (int c = 0; c < NT; ++c) {
-          if (c < mv) {
-            const float v = half_of(acc[c / 2], c & 1) + b;
-            if (p.out_f32) *reinterpret_cast<float*>(dst) = v;
-            else *reinterpret_cast<__nv_bfloat16*>(dst) = __float2bfloat16_rn(v);
+          for (int c = 0; c < NT; ++c) {
+            if (c < mv) *reinterpret_cast<float*>(dst) = half_of(acc[c / 2], c & 1) + b;
+            dst += step;
+            asm volatile("" : "+l"(dst));
           }
-          dst += step;
-          asm volatile("" : "+l"(dst));
+        } else {
+#pragma unroll
+          for (int c = 0; c < NT; ++c) {
+            if (c < mv)
+              *reinterpret_cast<__nv_bfloat16*>(dst) =
+                  __float2bfloat16_rn(half_of(acc[c / 2], c & 1) + b);
+            dst += step;
+            asm volatile("" : "+l"(dst));
+          }
         }
       }
     } else {
-      const int64_t part = (int64_t)NT * rpt;         // a CTA has room for two parts of tiles
+      const int t0 = at.unit0 - at.kb, t1 = t0 + p.kbu;      // the tile's shared units
+      const int64_t part_size = (int64_t)NT * kRows;    // a CTA has room for two parts of tiles
       if (mine) {
-        float* dst = p.part + (2 * blockIdx.x + (u0 >= t0 ? 0 : 1)) * part + wrow;
+        const int mine0 = w4_first(p.share_units, p.share_grid, blockIdx.x);
+        float* dst = p.part + (2 * blockIdx.x + (mine0 >= t0 ? 0 : 1)) * part_size + wrow;
 #pragma unroll
         for (int c = 0; c < NT; ++c)
-          if (c < mv) dst[c * rpt] = half_of(acc[c / 2], c & 1);
+          if (c < mv) dst[c * kRows] = half_of(acc[c / 2], c & 1);
       }
       __threadfence();
       w4_sync();
-      const int c0 = w4_owner(p.units, gridDim.x, t0), c1 = w4_owner(p.units, gridDim.x, t1 - 1);
+      const int c0 = w4_owner(p.share_units, p.share_grid, t0);
+      const int c1 = w4_owner(p.share_units, p.share_grid, t1 - 1);
       if (tid == 0) sh->last = atomicAdd(p.count + tile, 1) == c1 - c0;
       w4_sync();
       if (sh->last) {
         __threadfence();
         // this thread's rows at every step'th token; the loads of 8 tokens are in flight at once
-        constexpr int step = 256 / rpt;
-        const int rr = tid & (rpt - 1), n = at.rowt * rpt + rr;
+        constexpr int step = 256 / kRows;
+        const int rr = tid & (kRows - 1), n = rowt * kRows + rr;
         const float b = n < p.N ? bias_of(n) : 0.f;
-        for (int m = tid / rpt; m < mv; m += 8 * step) {
+        for (int m = tid / kRows; m < mv; m += 8 * step) {
           float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
           for (int c = c0; c <= c1; ++c) {
-            const bool first = w4_first(p.units, gridDim.x, c) >= t0;
-            const float* src = p.part + (2 * c + (first ? 0 : 1)) * part + rr;
+            const bool first = w4_first(p.share_units, p.share_grid, c) >= t0;
+            const float* src = p.part + (2 * c + (first ? 0 : 1)) * part_size + rr;
             float x[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              x[e] = m + e * step < mv ? __ldcg(src + (m + e * step) * rpt) : 0.f;
+              x[e] = m + e * step < mv ? __ldcg(src + (m + e * step) * kRows) : 0.f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] += x[e];
           }
@@ -399,42 +487,32 @@ __device__ __noinline__ void w4_sum(const W4Params& p, const W4Cta& c, int nu) {
         }
       }
     }
-    if constexpr (KS == 4) w4_sync();                 // `red` is free again
-    clear();
+    if constexpr (KS == 4) w4_sync();                   // `red` is free again
   }
   if (!ok && lane == 0) report(p.ws, ETREE_ETIMEOUT, DET_WAIT_W4);
 }
 
-template <int NT, int KS>
+template <int NT, int KS, int GPB>
 __global__ void __launch_bounds__(kWThreads, 1)
 w4_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_x,
           const __grid_constant__ W4Params p) {
+  using Sh = W4Shape<NT, KS, GPB>;
+  constexpr int kStages = Sh::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
+  float* red = reinterpret_cast<float*>(smem + kStages * Sh::kStage);      // [NT][128], KS = 4
+  W4Smem* sh = reinterpret_cast<W4Smem*>(reinterpret_cast<uint8_t*>(red) + Sh::kRed);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int ks = KS;                                // k blocks of a unit: 4 or 2
-  constexpr int xbytes = NT * 256;                          // one k block of x: two boxes [NT][64]
-  constexpr int stage = 4 * kWBox + ks * xbytes;
-  float* red = reinterpret_cast<float*>(smem + p.stages * stage);      // [NT][128], ks = 4
-  // scales of a unit's blocks: [unit parity][block][group][128 rows]
-  const int gpb = 128 / p.group;                        // groups of a k block
-  float* scale_s = red + (ks == 4 ? NT * 128 : 0);
-  W4Smem* sh = reinterpret_cast<W4Smem*>(scale_s + 8 * 128 * gpb);
-  const int u0 = w4_first(p.units, gridDim.x, blockIdx.x);
-  const int nu = w4_first(p.units, gridDim.x, blockIdx.x + 1) - u0;
-  constexpr int rpt = ks == 4 ? 128 : 256;                // rows of a tile
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < p.stages; ++i) {
-      mbar_init(&sh->full[i], 1);
-      mbar_init(&sh->empty[i], 10);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&sh->full[i], 2);                       // TMA, the scale warp
+      mbar_init(&sh->empty[i], 18);                     // 8 unpacking and 8 summing warps, 2 MMA commits
     }
     for (int w = 0; w < 4; ++w) {
       mbar_init(&sh->a_full[w], 4);
       mbar_init(&sh->a_free[w], 1);
-      mbar_init(&sh->s_full[w][0], 4);
-      mbar_init(&sh->s_full[w][1], 4);
       mbar_init(&sh->d_full[w], 1);
       mbar_init(&sh->d_free[w], 4);
     }
@@ -451,108 +529,104 @@ w4_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sh->tmem;                       // A of warpgroup w at 64 w, D at 256 + 64 w
+  const uint32_t tmem = sh->tmem;                       // block w: A at 64 w, D at 256 + 64 w
 
-  const int per_round = NT == 64 ? 1 : min(gpb, 64 / NT);          // groups that D holds at once
-  const int rounds = gpb / per_round;
-
-  const W4Cta c{smem, red, scale_s, sh, u0, tmem};
   if (warp == 0) {
     // ------------------------------------------------------------------------ TMA producer
     if (lane == 0) {
-      auto load_q = [&](const W4Walk& at, int st) {
-        const int kb = at.kb * ks, row0 = at.rowt * rpt;
-        uint8_t* dst = smem + st * stage;
-        mbar_arrive_expect_tx(&sh->full[st], stage);
+      auto load_q = [&](int rowt, int kb, int st) {
+        uint8_t* dst = smem + st * Sh::kStage;
+        mbar_arrive_expect_tx(&sh->full[st], Sh::kTx);
 #pragma unroll
         for (int w = 0; w < 4; ++w)
-          tma_load_2d(dst + w * kWBox, &tm_q, &sh->full[st], (kb + w % ks) * 64,
-                      row0 + w / ks * 128);
+          tma_load_2d(dst + w * kWBox, &tm_q, &sh->full[st], (kb * KS + w % KS) * 64,
+                      rowt * Sh::kRows + w / KS * 128);
       };
-      auto load_x = [&](const W4Walk& at, int st) {
-        uint8_t* dst = smem + st * stage + 4 * kWBox;
-        for (int w = 0; w < ks; ++w)
-          for (int h = 0; h < 2; ++h)
-            tma_load_2d(dst + w * xbytes + h * (NT * 128), &tm_x, &sh->full[st],
-                        (at.kb * ks + w) * 128 + h * 64, at.chunk * NT);
+      auto load_x = [&](int chunk, int kb, int st) {
+        uint8_t* dst = smem + st * Sh::kStage + 4 * kWBox;
+#pragma unroll
+        for (int w = 0; w < 2 * KS; ++w)
+          tma_load_2d(dst + w * (NT * 128), &tm_x, &sh->full[st], kb * KS * 128 + w * 64, chunk * NT);
       };
       // the first weights do not depend on the kernel that reorders x
-      const int ahead = min(nu, p.stages);
-      W4Walk at(p, u0);
-      for (int i = 0; i < ahead; ++i, at.next(p)) load_q(at, i);
+      int ahead = 0;
+      W4Segment at;
+      for (int seg = 0; ahead < kStages && w4_segment(p, seg, at); ++seg)
+        for (int i = 0; i < at.n && ahead < kStages; ++i) load_q(at.rowt, at.kb + i, ahead++);
       pdl_wait();
       bool ok = true;
       int issued = 0, st = 0;
       uint32_t ph = 0;
-      at = W4Walk(p, u0);
-      for (int i = 0; i < nu; ++i, at.next(p)) {
-        if (i >= ahead) {
-          if (!mbar_wait(&sh->empty[st], ph ^ 1)) { ok = false; break; }
-          load_q(at, st);
+      for (int seg = 0; ok && w4_segment(p, seg, at); ++seg)
+        for (int i = 0; i < at.n; ++i) {
+          if (issued >= ahead) {
+            if (!mbar_wait(&sh->empty[st], ph ^ 1)) { ok = false; break; }
+            load_q(at.rowt, at.kb + i, st);
+          }
+          load_x(at.chunk, at.kb + i, st);
+          ++issued;
+          if (++st == kStages) { st = 0; ph ^= 1; }
         }
-        load_x(at, st);
-        issued = i + 1;
-        if (++st == p.stages) { st = 0; ph ^= 1; }
-      }
-      // every copy has landed before the CTA may exit (bounded)
-      for (int i = max(0, issued - p.stages); i < issued; ++i)
-        ok = mbar_wait(&sh->full[i % p.stages], (i / p.stages) & 1) && ok;
+      // every copy has landed before the CTA may exit (bounded); weights without their x as well
+      // are none: the loop above reaches every unit that was loaded ahead
+      for (int i = max(0, issued - kStages); i < issued; ++i)
+        ok = mbar_wait(&sh->full[i % kStages], (i / kStages) & 1) && ok;
       if (!ok) report(p.ws, ETREE_ETIMEOUT, DET_WAIT_W4);
     }
   } else if (warp == 1 || warp == 2) {
     // ------------------------------------------------- MMA issuers, two of the four blocks each
-    const uint32_t id = idesc_bf16_f32(128, NT);
+    constexpr uint32_t id = idesc_bf16_f32(128, NT);
+    constexpr int kg = 8 / GPB;                         // MMAs of a group
     const uint64_t dx0 = smem_desc_sw128(smem + 4 * kWBox);
-    const int kg = p.group / 16, kg_log = 31 - __clz(kg);           // MMAs of a group
-    bool ok = true;
+    bool ok = true, any = false;
     int st = 0;
-    uint32_t ph = 0, use = 0;                           // `use` counts the fillings of D
-    for (int i = 0; ok && i < nu; ++i) {
-      ok = mbar_wait(&sh->full[st], ph);
-      tc_fence_after();
-      const uint64_t dx = dx0 + (uint64_t)((uint32_t)(st * stage) >> 4);
-      for (int rd = 0; rd < rounds; ++rd, ++use) {
+    uint32_t ph = 0, use = 0, unit = 0;                 // `use` counts the fillings of D
+    const int nu = units_of(p);
+      for (int i = 0; ok && i < nu; ++i) {
+        ok = mbar_wait(&sh->full[st], ph);
+        const uint64_t dx = dx0 + (uint64_t)((uint32_t)(st * Sh::kStage) >> 4);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int w = 2 * (warp - 1) + e;
-          if (use > 0) ok = ok && mbar_wait(&sh->d_free[w], (use - 1) & 1);
-          if (rd == 0) ok = ok && mbar_wait(&sh->a_full[w], i & 1);
-          tc_fence_after();
-          const uint64_t dxw = dx + w % ks * (xbytes >> 4);
-          const uint32_t aw = tmem + 64 * w, dw = aw + 256;
-          if (ok && elect_one()) {
-            if (kg == 8) {
+        for (int rd = 0; rd < Sh::kRounds; ++rd) {
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-                tc_mma_bf16_ts(dw, aw + 8 * k, dxw + (k >> 2) * (NT * 128 >> 4) + 2 * (k & 3), id,
-                               k > 0 ? 1u : 0u);
-            } else {
-              const int k0 = rd * per_round * kg;
-#pragma unroll 2
-              for (int k = 0; k < per_round * kg; ++k)
-                tc_mma_bf16_ts(dw + ((k >> kg_log) * NT), aw + 8 * (k0 + k),
-                               dxw + ((k0 + k) >> 2) * (NT * 128 >> 4) + 2 * ((k0 + k) & 3), id,
-                               k & (kg - 1));
+          for (int e = 0; e < 2; ++e) {
+            const int w = 2 * (warp - 1) + e;
+            if (any || rd > 0) ok = ok && mbar_wait(&sh->d_free[w], (use + rd - 1) & 1);
+            if (rd == 0) ok = ok && mbar_wait(&sh->a_full[w], unit & 1);
+            tc_fence_after();
+            const uint64_t dxw = dx + w % KS * (Sh::kX >> 4);
+            const uint32_t aw = tmem + 64 * w, dw = aw + 256;
+            if (ok && elect_one()) {
+#pragma unroll
+              for (int j = 0; j < Sh::kPerRound * kg; ++j) {
+                const int k = rd * Sh::kPerRound * kg + j;
+                tc_mma_bf16_ts(dw + j / kg * NT, aw + 8 * k,
+                               dxw + (k >> 2) * (NT * 128 >> 4) + 2 * (k & 3), id,
+                               j % kg > 0 ? 1u : 0u);
+              }
+              tc_commit(&sh->d_full[w]);
+              if (rd == Sh::kRounds - 1) {
+                tc_commit(&sh->a_free[w]);
+                if (e == 1) tc_commit(&sh->empty[st]);
+              }
             }
-            tc_commit(&sh->d_full[w]);
-            if (rd == rounds - 1) {
-              tc_commit(&sh->a_free[w]);
-              if (e == 1) tc_commit(&sh->empty[st]);
-            }
+            __syncwarp();
           }
-          __syncwarp();
         }
+        any = true;
+        use += Sh::kRounds;
+        ++unit;
+        if (++st == kStages) { st = 0; ph ^= 1; }
       }
-      if (++st == p.stages) { st = 0; ph ^= 1; }
-    }
     if (elect_one()) tc_commit(&sh->drain[warp - 1]);
     __syncwarp();
     if (!mbar_wait(&sh->drain[warp - 1], 0)) ok = false;
     if (!ok && lane == 0) report(p.ws, ETREE_ETIMEOUT, DET_WAIT_W4);
-  } else if (warp >= 4 && warp < 12) {
-    w4_unpack<NT, KS>(p, c, nu);
-  } else if (warp >= 12) {
-    w4_sum<NT, KS>(p, c, nu);
+  } else if (warp == 3) {
+    w4_scales<NT, KS, GPB>(p, smem, sh);
+  } else if (warp < 12) {
+    w4_unpack<NT, KS, GPB>(p, smem, sh, tmem, units_of(p));
+  } else {
+    w4_sum<NT, KS, GPB>(p, smem, red, sh, tmem);
   }
   tc_fence_before();
   __syncthreads();
@@ -562,28 +636,34 @@ w4_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
   }
 }
 
-static int w4_stages(int nt, int ks, int group) {
-  const int stage = 4 * kWBox + ks * nt * 256;
-  const int fixed = 1024 + (ks == 4 ? nt * 512 : 0) + 8 * 512 * (128 / group) + (int)sizeof(W4Smem);
-  return std::min(kWMaxStages, (kWSmem - fixed) / stage);
+template <int NT, int KS, int GPB>
+static cudaError_t go_w4(const CUtensorMap& q, const CUtensorMap& x, const W4Params& p, int grid,
+                         cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(w4_kernel<NT, KS, GPB>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kWSmem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(w4_kernel<NT, KS, GPB>, dim3(grid), dim3(kWThreads), (size_t)kWSmem, s, q, x, p);
 }
 
-cudaError_t launch_w4(const CUtensorMap& q, const CUtensorMap& x, W4Params p, int nt, int grid,
-                      cudaStream_t s) {
-  p.stages = w4_stages(nt, p.ks, p.group);
+template <int NT, int KS>
+static cudaError_t go_w4(const CUtensorMap& q, const CUtensorMap& x, const W4Params& p, int grid,
+                         cudaStream_t s) {
+  if (p.group == 128) return go_w4<NT, KS, 1>(q, x, p, grid, s);
+  if (p.group == 64) return go_w4<NT, KS, 2>(q, x, p, grid, s);
+  return go_w4<NT, KS, 4>(q, x, p, grid, s);
+}
+
+cudaError_t launch_w4(const CUtensorMap& q, const CUtensorMap& x, const W4Params& p, int nt, int ks,
+                      int grid, cudaStream_t s) {
   const int rows = p.chunks * nt;
   const int64_t items = (int64_t)rows * (p.K / 8);
   w4_prepare_kernel<<<(unsigned)((items + 255) / 256), 256, 0, s>>>(p, rows);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  auto go = [&](auto kernel) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWSmem);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(kernel, dim3(grid), dim3(kWThreads), (size_t)kWSmem, s, q, x, p);
-  };
-  if (p.ks == 4)
-    return nt == 16 ? go(w4_kernel<16, 4>) : go(w4_kernel<32, 4>);
-  return nt == 16 ? go(w4_kernel<16, 2>) : nt == 32 ? go(w4_kernel<32, 2>) : go(w4_kernel<64, 2>);
+  if (ks == 4) return nt == 16 ? go_w4<16, 4>(q, x, p, grid, s) : go_w4<32, 4>(q, x, p, grid, s);
+  return nt == 16   ? go_w4<16, 2>(q, x, p, grid, s)
+         : nt == 32 ? go_w4<32, 2>(q, x, p, grid, s)
+                    : go_w4<64, 2>(q, x, p, grid, s);
 }
 
 }  // namespace etree
