@@ -859,6 +859,9 @@ struct W4Plan {
   size_t count, xp, part, total;
 };
 
+// Up to this many tokens take the kernel without tensor memory.
+constexpr int kW4Small = 16;
+
 // Tokens go in chunks of 16, 32 or 64.  Units of two row tiles read x once for 256 rows and are
 // taken where they fill the SMs; with fewer rows a unit is four k blocks of one row tile.
 static W4Plan plan_w4(int M, int N, int K) {          // checked arguments: units fit 32 bits
@@ -922,35 +925,41 @@ etree_status etree_w4_linear(const uint16_t* x, int64_t x_stride, int M, const u
     return fail(ETREE_EINVAL, "workspace is NULL or not 256-byte aligned");
   if (workspace_bytes < pl.total)
     return fail(ETREE_EINVAL, "workspace has %zu bytes, needs %zu", workspace_bytes, pl.total);
-  CUtensorMap tq, tx;
-  if ((st = get_map_w4(wq, K / 2, N, &tq))) return st;
-  if ((st = get_map(at<uint16_t>(workspace, pl.xp), 2, K, (uint64_t)pl.chunks * pl.nt, 1, 64,
-                    pl.nt, 1, &tx)))
-    return st;
   W4Params p{};
   p.x = x;
   p.x_stride = x_stride;
+  p.wq = wq;
   p.scales = scales;
   p.zeros = zeros;
   p.bias = bias;
   p.out = out;
   p.out_stride = out_stride;
   p.out_f32 = out_f32;
-  p.xp = at<uint16_t>(workspace, pl.xp);
-  p.part = at<float>(workspace, pl.part);
-  p.count = at<int32_t>(workspace, pl.count);
   p.ws = at<WsHeader>(workspace, 0);
   p.M = M;
   p.N = N;
   p.K = K;
   p.group = group;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (M <= kW4Small) {
+    const cudaError_t e = launch_w4_small(p, N >= 64 * sm_count() ? 2 : 1, s);
+    return e == cudaSuccess ? ETREE_OK : cuda_fail(e, "etree_w4_linear launch");
+  }
+  CUtensorMap tq, tx;
+  if ((st = get_map_w4(wq, K / 2, N, &tq))) return st;
+  if ((st = get_map(at<uint16_t>(workspace, pl.xp), 2, K, (uint64_t)pl.chunks * pl.nt, 1, 64,
+                    pl.nt, 1, &tx)))
+    return st;
+  p.xp = at<uint16_t>(workspace, pl.xp);
+  p.part = at<float>(workspace, pl.part);
+  p.count = at<int32_t>(workspace, pl.count);
   p.kbu = pl.kbu;
   p.chunks = pl.chunks;
   p.tiles = pl.tiles;
   p.whole = pl.whole;
   p.share_units = pl.share_units;
   p.share_grid = pl.share_grid;
-  cudaError_t e = launch_w4(tq, tx, p, pl.nt, pl.ks, pl.grid, static_cast<cudaStream_t>(stream));
+  cudaError_t e = launch_w4(tq, tx, p, pl.nt, pl.ks, pl.grid, s);
   return e == cudaSuccess ? ETREE_OK : cuda_fail(e, "etree_w4_linear launch");
 }
 

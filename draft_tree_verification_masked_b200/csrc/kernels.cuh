@@ -217,6 +217,7 @@ cudaError_t launch_kv_store(const StoreParams& p, cudaStream_t s);
 // Products with 4-bit weights (w4.cu).
 struct W4Params {
   const uint16_t* x;                // bf16 bits, rows x_stride elements apart
+  const uint8_t* wq;                // [N][K / 2]
   const uint16_t* scales;           // [N][K / group] bf16 bits
   const uint8_t* zeros;             // [N][K / group], or null: 8
   const uint16_t* bias;             // [N] bf16 bits, or null
@@ -230,6 +231,7 @@ struct W4Params {
   int kbu, chunks, tiles;           // units a tile, token chunks, tiles
   int whole, share_units, share_grid;   // whole tiles a CTA; the other tiles' units, and their CTAs
 };
+cudaError_t launch_w4_small(const W4Params& p, int mt, cudaStream_t s);
 cudaError_t launch_w4(const CUtensorMap& q, const CUtensorMap& x, const W4Params& p, int nt, int ks,
                       int grid, cudaStream_t s);
 

@@ -636,6 +636,179 @@ w4_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
   }
 }
 
+// Few tokens (at most 16): one launch, no tensor memory, no reordered x.  A warp takes MT x 16 rows
+// at every eighth k block and multiplies with mma.sync m16n8k16 (weights as A, NTL x 8 tokens as
+// B); the order of k inside a block is free as long as A and B agree, so a lane loads its rows'
+// bytes and its token's values in runs, in words of eight weights whose k lie in one group:
+//   word w of lane t (of the four that share a row) starts at k = first(w, t),
+//   GPB = 1: 32 t + 8 w;   2: 64 (w / 2) + 16 t + 8 (w % 2);   4: 32 w + 8 t.
+// Sums of a group leave the tensor core as they do above and are scaled in fp32; the eight warps'
+// sums meet in shared memory in the order of the warps.
+constexpr int kSmallWarps = 8;
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int MT, int GPB>
+struct W4SmallBlock {                                   // a lane's part of MT x 16 rows x 128 k
+  uint32_t q[MT][2][4];                                 // [tile][row g or g + 8][word]
+  uint16_t s[MT][2][GPB];
+  uint8_t z[MT][2][GPB];
+};
+
+template <int MT, int NTL, int GPB>
+__global__ void __launch_bounds__(32 * kSmallWarps) w4_small_kernel(const __grid_constant__ W4Params p) {
+  constexpr int kRows = 16 * MT, kTok = 8 * NTL;
+  __shared__ float sums[kSmallWarps][kTok][kRows + 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int n0 = blockIdx.x * kRows, nkb = (p.K + 127) / 128, ng = p.K / p.group;
+  const int64_t qstride = p.K / 2;
+  auto first = [&](int w) {
+    return GPB == 1 ? 32 * t + 8 * w : GPB == 2 ? 64 * (w / 2) + 16 * t + 8 * (w % 2) : 32 * w + 8 * t;
+  };
+  auto load = [&](W4SmallBlock<MT, GPB>& blk, int kb) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int n = min(n0 + 16 * i + 8 * h + g, p.N - 1);       // rows behind the end: any row
+        const uint8_t* row = p.wq + n * qstride + kb * 64;
+        constexpr int kRun = 4 / GPB;                   // words that lie together
+#pragma unroll
+        for (int w = 0; w < 4; w += kRun) {
+          const int k = first(w);
+          uint32_t* dst = &blk.q[i][h][w];
+          if (kb * 128 + k < p.K) {
+            if constexpr (GPB == 1) {
+              const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + k / 2));
+              dst[0] = v.x;
+              dst[1] = v.y;
+              dst[2] = v.z;
+              dst[3] = v.w;
+            } else if constexpr (GPB == 2) {
+              const uint2 v = __ldg(reinterpret_cast<const uint2*>(row + k / 2));
+              dst[0] = v.x;
+              dst[1] = v.y;
+            } else {
+              dst[0] = __ldg(reinterpret_cast<const uint32_t*>(row + k / 2));
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < kRun; ++j) dst[j] = 0u;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < GPB; ++j) {
+          const int64_t at = (int64_t)n * ng + min(kb * GPB + j, ng - 1);
+          blk.s[i][h][j] = __ldg(p.scales + at);
+          blk.z[i][h][j] = p.zeros ? __ldg(p.zeros + at) : 8;
+        }
+      }
+  };
+  W4SmallBlock<MT, GPB> cur, nxt;
+  if (warp < nkb) load(cur, warp);                      // weights do not depend on earlier kernels
+  pdl_wait();
+  pdl_trigger();
+  float acc[MT][NTL][4] = {};
+  for (int kb = warp; kb < nkb; kb += kSmallWarps) {
+    uint4 x[NTL][4];
+#pragma unroll
+    for (int j = 0; j < NTL; ++j) {
+      const int m = 8 * j + g;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const int k = kb * 128 + first(w);
+        x[j][w] = m < p.M && k < p.K
+                      ? __ldg(reinterpret_cast<const uint4*>(p.x + m * p.x_stride + k))
+                      : make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+    if (kb + kSmallWarps < nkb) load(nxt, kb + kSmallWarps);
+#pragma unroll
+    for (int gi = 0; gi < GPB; ++gi) {
+      float d[MT][NTL][4] = {};
+#pragma unroll
+      for (int w = gi * 4 / GPB; w < (gi + 1) * 4 / GPB; ++w)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {          // pairs (2 half, 2 half + 4), (.. + 1, .. + 5)
+          uint32_t b[NTL][2];
+#pragma unroll
+          for (int j = 0; j < NTL; ++j) {
+            const uint32_t lo = half ? x[j][w].y : x[j][w].x, hi = half ? x[j][w].w : x[j][w].z;
+            b[j][0] = __byte_perm(lo, hi, 0x5410);
+            b[j][1] = __byte_perm(lo, hi, 0x7632);
+          }
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+            uint32_t a[4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t zz = 0x43004300u | (cur.z[i][h][gi] & 15u) * 0x00010001u;
+              const uint32_t q = cur.q[i][h][w] >> (8 * half);
+              a[h] = sub_pair((q & 0x000f000fu) | 0x43004300u, zz);
+              a[2 + h] = sub_pair(((q >> 4) & 0x000f000fu) | 0x43004300u, zz);
+            }
+#pragma unroll
+            for (int j = 0; j < NTL; ++j) mma_bf16(d[i][j], a, b[j][0], b[j][1]);
+          }
+        }
+      if (kb * GPB + gi < ng) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          const float s0 = __uint_as_float((uint32_t)cur.s[i][0][gi] << 16);
+          const float s1 = __uint_as_float((uint32_t)cur.s[i][1][gi] << 16);
+#pragma unroll
+          for (int j = 0; j < NTL; ++j) {
+            acc[i][j][0] += s0 * d[i][j][0];
+            acc[i][j][1] += s0 * d[i][j][1];
+            acc[i][j][2] += s1 * d[i][j][2];
+            acc[i][j][3] += s1 * d[i][j][3];
+          }
+        }
+      }
+    }
+    cur = nxt;
+  }
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NTL; ++j)
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        sums[warp][8 * j + 2 * t + (c & 1)][16 * i + g + 8 * (c >> 1)] = acc[i][j][c];
+  __syncthreads();
+  for (int o = threadIdx.x; o < kRows * kTok; o += 32 * kSmallWarps) {
+    const int r = o % kRows, m = o / kRows, n = n0 + r;
+    if (n >= p.N || m >= p.M) continue;
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kSmallWarps; ++w) v += sums[w][m][r];
+    if (p.bias) v += __uint_as_float((uint32_t)__ldg(p.bias + n) << 16);
+    const int64_t at = m * p.out_stride + n;
+    if (p.out_f32) reinterpret_cast<float*>(p.out)[at] = v;
+    else reinterpret_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
+  }
+}
+
+template <int MT, int NTL>
+static cudaError_t go_w4_small(const W4Params& p, cudaStream_t s) {
+  const dim3 grid((p.N + 16 * MT - 1) / (16 * MT)), block(32 * kSmallWarps);
+  if (p.group == 128) return launch_pdl(w4_small_kernel<MT, NTL, 1>, grid, block, 0, s, p);
+  if (p.group == 64) return launch_pdl(w4_small_kernel<MT, NTL, 2>, grid, block, 0, s, p);
+  return launch_pdl(w4_small_kernel<MT, NTL, 4>, grid, block, 0, s, p);
+}
+
+cudaError_t launch_w4_small(const W4Params& p, int mt, cudaStream_t s) {
+  if (p.M <= 8) return mt == 1 ? go_w4_small<1, 1>(p, s) : go_w4_small<2, 1>(p, s);
+  return mt == 1 ? go_w4_small<1, 2>(p, s) : go_w4_small<2, 2>(p, s);
+}
+
 template <int NT, int KS, int GPB>
 static cudaError_t go_w4(const CUtensorMap& q, const CUtensorMap& x, const W4Params& p, int grid,
                          cudaStream_t s) {
