@@ -877,7 +877,9 @@ static W4Plan plan_w4(int M, int N, int K) {          // checked arguments: unit
   pl.grid = (int)std::min<int64_t>((int64_t)pl.tiles * pl.kbu, sms);
   pl.whole = pl.tiles / pl.grid;                       // the tiles left over are shared by units
   pl.share_units = (pl.tiles - pl.whole * pl.grid) * pl.kbu;
-  pl.share_grid = std::min(pl.share_units, pl.grid);
+  // about sqrt(kbu) units a CTA: fewer parts of a tile to add up against fewer units in turn
+  const int run = std::max(1, (int)std::lround(std::sqrt((double)pl.kbu)));
+  pl.share_grid = std::min((pl.share_units + run - 1) / run, pl.grid);
   pl.count = up256(sizeof(WsHeader));
   pl.xp = up256(pl.count + (size_t)pl.tiles * sizeof(int32_t));
   pl.part = up256(pl.xp + (size_t)pl.chunks * pl.nt * K * 2);
@@ -959,6 +961,8 @@ etree_status etree_w4_linear(const uint16_t* x, int64_t x_stride, int M, const u
   p.whole = pl.whole;
   p.share_units = pl.share_units;
   p.share_grid = pl.share_grid;
+  p.share_base = pl.share_units / std::max(1, pl.share_grid);
+  p.share_rem = pl.share_units % std::max(1, pl.share_grid);
   cudaError_t e = launch_w4(tq, tx, p, pl.nt, pl.ks, pl.grid, s);
   return e == cudaSuccess ? ETREE_OK : cuda_fail(e, "etree_w4_linear launch");
 }

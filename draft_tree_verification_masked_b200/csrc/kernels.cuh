@@ -230,6 +230,7 @@ struct W4Params {
   int M, N, K, group, out_f32;
   int kbu, chunks, tiles;           // units a tile, token chunks, tiles
   int whole, share_units, share_grid;   // whole tiles a CTA; the other tiles' units, and their CTAs
+  int share_base, share_rem;        // share_units = share_grid * share_base + share_rem
 };
 cudaError_t launch_w4_small(const W4Params& p, int mt, cudaStream_t s);
 cudaError_t launch_w4(const CUtensorMap& q, const CUtensorMap& x, const W4Params& p, int nt, int ks,

@@ -64,13 +64,14 @@ struct W4Shape {
 
 __device__ __forceinline__ void w4_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
-// The units of the shared tiles are dealt to the first `grid` CTAs: CTA c's first one, and the CTA
-// that holds unit u.
-__device__ __forceinline__ int w4_first(int units, int grid, int c) {
-  return (int)((int64_t)units * c / grid);
+// The units of the shared tiles are dealt to the first share_grid CTAs, share_base each and one more
+// to the first share_rem: CTA c's first unit, and the CTA that holds unit u.
+__device__ __forceinline__ int w4_first(const W4Params& p, int c) {
+  return c * p.share_base + min(c, p.share_rem);
 }
-__device__ __forceinline__ int w4_owner(int units, int grid, int u) {
-  return (int)(((int64_t)(u + 1) * grid - 1) / units);
+__device__ __forceinline__ int w4_owner(const W4Params& p, int u) {
+  const int longer = p.share_rem * (p.share_base + 1);
+  return u < longer ? u / (p.share_base + 1) : p.share_rem + (u - longer) / p.share_base;
 }
 
 // A CTA's segments in order: its share of the shared tiles' units, at most the end of one tile and
@@ -81,8 +82,8 @@ struct W4Segment {
 };
 __device__ __forceinline__ bool w4_segment(const W4Params& p, int s, W4Segment& at) {
   if ((int)blockIdx.x < p.share_grid) {
-    int u = w4_first(p.share_units, p.share_grid, blockIdx.x);
-    const int end = w4_first(p.share_units, p.share_grid, blockIdx.x + 1);
+    int u = w4_first(p, blockIdx.x);
+    const int end = w4_first(p, blockIdx.x + 1);
     int t = u / p.kbu;
     const int split = min(end, (t + 1) * p.kbu);
     if (s == 1 && split < end) {
@@ -116,8 +117,8 @@ __device__ __forceinline__ bool w4_segment(const W4Params& p, int s, W4Segment& 
 __device__ __forceinline__ int units_of(const W4Params& p) {
   const int own = p.whole * p.kbu;
   if ((int)blockIdx.x >= p.share_grid) return own;
-  return own + w4_first(p.share_units, p.share_grid, blockIdx.x + 1) -
-         w4_first(p.share_units, p.share_grid, blockIdx.x);
+  return own + w4_first(p, blockIdx.x + 1) -
+         w4_first(p, blockIdx.x);
 }
 
 __device__ __forceinline__ void tmem_st16_async(uint32_t taddr, const uint32_t (&v)[16]) {
@@ -445,7 +446,7 @@ __device__ __noinline__ void w4_sum(const W4Params& p, const uint8_t* smem, floa
       const int t0 = at.unit0 - at.kb, t1 = t0 + p.kbu;      // the tile's shared units
       const int64_t part_size = (int64_t)NT * kRows;    // a CTA has room for two parts of tiles
       if (mine) {
-        const int mine0 = w4_first(p.share_units, p.share_grid, blockIdx.x);
+        const int mine0 = w4_first(p, blockIdx.x);
         float* dst = p.part + (2 * blockIdx.x + (mine0 >= t0 ? 0 : 1)) * part_size + wrow;
 #pragma unroll
         for (int c = 0; c < NT; ++c)
@@ -453,35 +454,50 @@ __device__ __noinline__ void w4_sum(const W4Params& p, const uint8_t* smem, floa
       }
       __threadfence();
       w4_sync();
-      const int c0 = w4_owner(p.share_units, p.share_grid, t0);
-      const int c1 = w4_owner(p.share_units, p.share_grid, t1 - 1);
+      const int c0 = w4_owner(p, t0);
+      const int c1 = w4_owner(p, t1 - 1);
       if (tid == 0) sh->last = atomicAdd(p.count + tile, 1) == c1 - c0;
       w4_sync();
       if (sh->last) {
         __threadfence();
-        // this thread's rows at every step'th token; the loads of 8 tokens are in flight at once
-        constexpr int step = 256 / kRows;
-        const int rr = tid & (kRows - 1), n = rowt * kRows + rr;
-        const float b = n < p.N ? bias_of(n) : 0.f;
-        for (int m = tid / kRows; m < mv; m += 8 * step) {
-          float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-          for (int c = c0; c <= c1; ++c) {
-            const bool first = w4_first(p.share_units, p.share_grid, c) >= t0;
-            const float* src = p.part + (2 * c + (first ? 0 : 1)) * part_size + rr;
-            float x[8];
+        // four rows of one token a thread, and four parts' loads of two tokens in flight at once
+        constexpr int step = 256 / (kRows / 4);
+        const int rr = tid % (kRows / 4) * 4, n = rowt * kRows + rr;
+        for (int m = tid / (kRows / 4); m < mv; m += 2 * step) {
+          float4 v[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+          for (int c = c0; c <= c1; c += 4) {
+            float4 x[4][2];
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              x[e] = m + e * step < mv ? __ldcg(src + (m + e * step) * kRows) : 0.f;
+            for (int i = 0; i < 4; ++i) {
+              const bool first = w4_first(p, min(c + i, c1)) >= t0;
+              const float* src = p.part + (2 * min(c + i, c1) + (first ? 0 : 1)) * part_size + rr;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] += x[e];
+              for (int e = 0; e < 2; ++e)
+                x[i][e] = c + i <= c1 && m + e * step < mv
+                              ? __ldcg(reinterpret_cast<const float4*>(src + (m + e * step) * kRows))
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                v[e].x += x[i][e].x;
+                v[e].y += x[i][e].y;
+                v[e].z += x[i][e].z;
+                v[e].w += x[i][e].w;
+              }
           }
-          if (n < p.N) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (m + e * step < mv) {
-                const int64_t o = (int64_t)(m0 + m + e * step) * p.out_stride + n;
-                if (p.out_f32) reinterpret_cast<float*>(p.out)[o] = v[e] + b;
-                else reinterpret_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(v[e] + b);
+          for (int e = 0; e < 2; ++e) {
+            if (m + e * step >= mv) continue;
+            const float y[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
+            const int64_t o = (int64_t)(m0 + m + e * step) * p.out_stride + n;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (n + i < p.N) {
+                const float r = y[i] + bias_of(n + i);
+                if (p.out_f32) reinterpret_cast<float*>(p.out)[o + i] = r;
+                else reinterpret_cast<__nv_bfloat16*>(p.out)[o + i] = __float2bfloat16_rn(r);
               }
           }
         }
@@ -664,39 +680,51 @@ struct W4SmallBlock {                                   // a lane's part of MT x
 
 template <int MT, int NTL, int GPB>
 __global__ void __launch_bounds__(32 * kSmallWarps) w4_small_kernel(const __grid_constant__ W4Params p) {
-  constexpr int kRows = 16 * MT, kTok = 8 * NTL;
-  __shared__ float sums[kSmallWarps][kTok][kRows + 1];
+  constexpr int kRows = 16 * MT, kPart = NTL < 4 ? NTL : 4, kTok = 8 * kPart;
+  __shared__ float sums[kSmallWarps][kTok][kRows + 1];  // kPart of the NTL token tiles at once
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int n0 = blockIdx.x * kRows, nkb = (p.K + 127) / 128, ng = p.K / p.group;
-  const int64_t qstride = p.K / 2;
+  uint32_t magic = 0x43004300u;
+  asm volatile("" : "+r"(magic));                       // stays in a register
   auto first = [&](int w) {
     return GPB == 1 ? 32 * t + 8 * w : GPB == 2 ? 64 * (w / 2) + 16 * t + 8 * (w % 2) : 32 * w + 8 * t;
   };
+  const uint8_t* qrow[MT][2];
+  const uint16_t* srow[MT][2];
+  const uint8_t* zrow[MT][2];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t n = min(n0 + 16 * i + 8 * h + g, p.N - 1);     // rows behind the end: any row
+      qrow[i][h] = p.wq + n * (p.K / 2);
+      srow[i][h] = p.scales + n * ng;
+      zrow[i][h] = p.zeros + n * ng;
+    }
   auto load = [&](W4SmallBlock<MT, GPB>& blk, int kb) {
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int n = min(n0 + 16 * i + 8 * h + g, p.N - 1);       // rows behind the end: any row
-        const uint8_t* row = p.wq + n * qstride + kb * 64;
         constexpr int kRun = 4 / GPB;                   // words that lie together
 #pragma unroll
         for (int w = 0; w < 4; w += kRun) {
-          const int k = first(w);
+          const int k = kb * 128 + first(w);
+          const uint8_t* at = qrow[i][h] + k / 2;
           uint32_t* dst = &blk.q[i][h][w];
-          if (kb * 128 + k < p.K) {
+          if (k < p.K) {
             if constexpr (GPB == 1) {
-              const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + k / 2));
+              const uint4 v = __ldg(reinterpret_cast<const uint4*>(at));
               dst[0] = v.x;
               dst[1] = v.y;
               dst[2] = v.z;
               dst[3] = v.w;
             } else if constexpr (GPB == 2) {
-              const uint2 v = __ldg(reinterpret_cast<const uint2*>(row + k / 2));
+              const uint2 v = __ldg(reinterpret_cast<const uint2*>(at));
               dst[0] = v.x;
               dst[1] = v.y;
             } else {
-              dst[0] = __ldg(reinterpret_cast<const uint32_t*>(row + k / 2));
+              dst[0] = __ldg(reinterpret_cast<const uint32_t*>(at));
             }
           } else {
 #pragma unroll
@@ -705,64 +733,57 @@ __global__ void __launch_bounds__(32 * kSmallWarps) w4_small_kernel(const __grid
         }
 #pragma unroll
         for (int j = 0; j < GPB; ++j) {
-          const int64_t at = (int64_t)n * ng + min(kb * GPB + j, ng - 1);
-          blk.s[i][h][j] = __ldg(p.scales + at);
-          blk.z[i][h][j] = p.zeros ? __ldg(p.zeros + at) : 8;
+          const int at = min(kb * GPB + j, ng - 1);
+          blk.s[i][h][j] = __ldg(srow[i][h] + at);
+          blk.z[i][h][j] = p.zeros ? __ldg(zrow[i][h] + at) : 8;
         }
       }
   };
-  W4SmallBlock<MT, GPB> cur, nxt;
-  if (warp < nkb) load(cur, warp);                      // weights do not depend on earlier kernels
-  pdl_wait();
-  pdl_trigger();
   float acc[MT][NTL][4] = {};
-  for (int kb = warp; kb < nkb; kb += kSmallWarps) {
-    uint4 x[NTL][4];
-#pragma unroll
-    for (int j = 0; j < NTL; ++j) {
-      const int m = 8 * j + g;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const int k = kb * 128 + first(w);
-        x[j][w] = m < p.M && k < p.K
-                      ? __ldg(reinterpret_cast<const uint4*>(p.x + m * p.x_stride + k))
-                      : make_uint4(0u, 0u, 0u, 0u);
-      }
-    }
-    if (kb + kSmallWarps < nkb) load(nxt, kb + kSmallWarps);
+  const uint16_t* xrow = p.x + g * p.x_stride;          // token g, and every eighth after it
+  auto multiply = [&](const W4SmallBlock<MT, GPB>& blk, int kb) {
 #pragma unroll
     for (int gi = 0; gi < GPB; ++gi) {
       float d[MT][NTL][4] = {};
+      uint32_t zz[MT][2];
 #pragma unroll
-      for (int w = gi * 4 / GPB; w < (gi + 1) * 4 / GPB; ++w)
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) zz[i][h] = (blk.z[i][h][gi] & 15u) * 0x00010001u | magic;
+#pragma unroll
+      for (int w = gi * 4 / GPB; w < (gi + 1) * 4 / GPB; ++w) {
+        uint4 x[NTL];
+        const int k = kb * 128 + first(w);
+#pragma unroll
+        for (int j = 0; j < NTL; ++j)
+          x[j] = 8 * j + g < p.M && k < p.K
+                     ? __ldg(reinterpret_cast<const uint4*>(xrow + 8 * j * p.x_stride + k))
+                     : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {          // pairs (2 half, 2 half + 4), (.. + 1, .. + 5)
-          uint32_t b[NTL][2];
+          uint32_t a[MT][4];
 #pragma unroll
-          for (int j = 0; j < NTL; ++j) {
-            const uint32_t lo = half ? x[j][w].y : x[j][w].x, hi = half ? x[j][w].w : x[j][w].z;
-            b[j][0] = __byte_perm(lo, hi, 0x5410);
-            b[j][1] = __byte_perm(lo, hi, 0x7632);
-          }
-#pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            uint32_t a[4];
+          for (int i = 0; i < MT; ++i)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const uint32_t zz = 0x43004300u | (cur.z[i][h][gi] & 15u) * 0x00010001u;
-              const uint32_t q = cur.q[i][h][w] >> (8 * half);
-              a[h] = sub_pair((q & 0x000f000fu) | 0x43004300u, zz);
-              a[2 + h] = sub_pair(((q >> 4) & 0x000f000fu) | 0x43004300u, zz);
+              const uint32_t q = blk.q[i][h][w] >> (8 * half);
+              a[i][h] = sub_pair(nibble_pair(q, magic), zz[i][h]);
+              a[i][2 + h] = sub_pair(nibble_pair(blk.q[i][h][w] >> (8 * half + 4), magic), zz[i][h]);
             }
 #pragma unroll
-            for (int j = 0; j < NTL; ++j) mma_bf16(d[i][j], a, b[j][0], b[j][1]);
+          for (int j = 0; j < NTL; ++j) {
+            const uint32_t lo = half ? x[j].y : x[j].x, hi = half ? x[j].w : x[j].z;
+            const uint32_t b0 = __byte_perm(lo, hi, 0x5410), b1 = __byte_perm(lo, hi, 0x7632);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) mma_bf16(d[i][j], a[i], b0, b1);
           }
         }
+      }
       if (kb * GPB + gi < ng) {
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
-          const float s0 = __uint_as_float((uint32_t)cur.s[i][0][gi] << 16);
-          const float s1 = __uint_as_float((uint32_t)cur.s[i][1][gi] << 16);
+          const float s0 = __uint_as_float((uint32_t)blk.s[i][0][gi] << 16);
+          const float s1 = __uint_as_float((uint32_t)blk.s[i][1][gi] << 16);
 #pragma unroll
           for (int j = 0; j < NTL; ++j) {
             acc[i][j][0] += s0 * d[i][j][0];
@@ -773,26 +794,43 @@ __global__ void __launch_bounds__(32 * kSmallWarps) w4_small_kernel(const __grid
         }
       }
     }
-    cur = nxt;
+  };
+  W4SmallBlock<MT, GPB> even, odd;
+  int kb = warp;
+  if (kb < nkb) load(even, kb);                         // weights do not depend on earlier kernels
+  pdl_wait();
+  pdl_trigger();
+  while (kb < nkb) {
+    if (kb + kSmallWarps < nkb) load(odd, kb + kSmallWarps);
+    multiply(even, kb);
+    kb += kSmallWarps;
+    if (kb >= nkb) break;
+    if (kb + kSmallWarps < nkb) load(even, kb + kSmallWarps);
+    multiply(odd, kb);
+    kb += kSmallWarps;
   }
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
+  for (int j0 = 0; j0 < NTL; j0 += kPart) {
+    if (j0 > 0) __syncthreads();
 #pragma unroll
-    for (int j = 0; j < NTL; ++j)
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        sums[warp][8 * j + 2 * t + (c & 1)][16 * i + g + 8 * (c >> 1)] = acc[i][j][c];
-  __syncthreads();
-  for (int o = threadIdx.x; o < kRows * kTok; o += 32 * kSmallWarps) {
-    const int r = o % kRows, m = o / kRows, n = n0 + r;
-    if (n >= p.N || m >= p.M) continue;
-    float v = 0.f;
+      for (int j = 0; j < kPart; ++j)
 #pragma unroll
-    for (int w = 0; w < kSmallWarps; ++w) v += sums[w][m][r];
-    if (p.bias) v += __uint_as_float((uint32_t)__ldg(p.bias + n) << 16);
-    const int64_t at = m * p.out_stride + n;
-    if (p.out_f32) reinterpret_cast<float*>(p.out)[at] = v;
-    else reinterpret_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
+        for (int c = 0; c < 4; ++c)
+          sums[warp][8 * j + 2 * t + (c & 1)][16 * i + g + 8 * (c >> 1)] = acc[i][j0 + j][c];
+    __syncthreads();
+    for (int o = threadIdx.x; o < kRows * kTok; o += 32 * kSmallWarps) {
+      const int r = o % kRows, m = 8 * j0 + o / kRows, n = n0 + r;
+      if (n >= p.N || m >= p.M) continue;
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < kSmallWarps; ++w) v += sums[w][o / kRows][r];
+      if (p.bias) v += __uint_as_float((uint32_t)__ldg(p.bias + n) << 16);
+      const int64_t at = m * p.out_stride + n;
+      if (p.out_f32) reinterpret_cast<float*>(p.out)[at] = v;
+      else reinterpret_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
+    }
   }
 }
 
@@ -806,7 +844,9 @@ static cudaError_t go_w4_small(const W4Params& p, cudaStream_t s) {
 
 cudaError_t launch_w4_small(const W4Params& p, int mt, cudaStream_t s) {
   if (p.M <= 8) return mt == 1 ? go_w4_small<1, 1>(p, s) : go_w4_small<2, 1>(p, s);
-  return mt == 1 ? go_w4_small<1, 2>(p, s) : go_w4_small<2, 2>(p, s);
+  if (p.M <= 16) return mt == 1 ? go_w4_small<1, 2>(p, s) : go_w4_small<2, 2>(p, s);
+  if (p.M <= 32) return mt == 1 ? go_w4_small<1, 4>(p, s) : go_w4_small<2, 4>(p, s);
+  return mt == 1 ? go_w4_small<1, 8>(p, s) : go_w4_small<2, 8>(p, s);
 }
 
 template <int NT, int KS, int GPB>
