@@ -856,11 +856,19 @@ etree_status etree_verify_attn_diff_paged(
 // ------------------------------------------------------------------ products with 4-bit weights
 struct W4Plan {
   int nt, ks, chunks, kbu, tiles, grid, whole, share_units, share_grid;
-  size_t count, xp, part, total;
+  size_t xp, part, total;
 };
 
-// Up to this many tokens take the kernel without tensor memory.
-constexpr int kW4Small = 16;
+// The one-launch kernel serves up to 8 tokens always (8 tokens of 40000 x 8192: 66 us against 84),
+// and up to 64 while (tokens, in tiles of 8) x N x K is small, where it saves the other's start
+// (64 tokens of 1000 x 2048: 6 us against 19).  Measured crossings lie between 40 M and 65 M weights
+// at 16 tokens, 20 M and 37 M at 32, and 8 M and 20 M at 64.
+static bool w4_is_small(int M, int N, int K) {
+  if (M <= 8) return true;
+  if (M > 64) return false;
+  const int tokens = M <= 16 ? 16 : M <= 32 ? 32 : 64;
+  return (int64_t)tokens * N * K <= (int64_t)800 << 20;
+}
 
 // Tokens go in chunks of 16, 32 or 64.  Units of two row tiles read x once for 256 rows and are
 // taken where they fill the SMs; with fewer rows a unit is four k blocks of one row tile.
@@ -880,8 +888,7 @@ static W4Plan plan_w4(int M, int N, int K) {          // checked arguments: unit
   // about sqrt(kbu) units a CTA: fewer parts of a tile to add up against fewer units in turn
   const int run = std::max(1, (int)std::lround(std::sqrt((double)pl.kbu)));
   pl.share_grid = std::min((pl.share_units + run - 1) / run, pl.grid);
-  pl.count = up256(sizeof(WsHeader));
-  pl.xp = up256(pl.count + (size_t)pl.tiles * sizeof(int32_t));
+  pl.xp = up256(sizeof(WsHeader));
   pl.part = up256(pl.xp + (size_t)pl.chunks * pl.nt * K * 2);
   pl.total = up256(pl.part + (size_t)2 * pl.grid * pl.nt * rpt * sizeof(float));
   return pl;
@@ -943,7 +950,7 @@ etree_status etree_w4_linear(const uint16_t* x, int64_t x_stride, int M, const u
   p.K = K;
   p.group = group;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (M <= kW4Small) {
+  if (w4_is_small(M, N, K)) {
     const cudaError_t e = launch_w4_small(p, N >= 64 * sm_count() ? 2 : 1, s);
     return e == cudaSuccess ? ETREE_OK : cuda_fail(e, "etree_w4_linear launch");
   }
@@ -954,7 +961,6 @@ etree_status etree_w4_linear(const uint16_t* x, int64_t x_stride, int M, const u
     return st;
   p.xp = at<uint16_t>(workspace, pl.xp);
   p.part = at<float>(workspace, pl.part);
-  p.count = at<int32_t>(workspace, pl.count);
   p.kbu = pl.kbu;
   p.chunks = pl.chunks;
   p.tiles = pl.tiles;

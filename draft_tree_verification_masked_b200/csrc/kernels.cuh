@@ -224,7 +224,6 @@ struct W4Params {
   void* out;                        // bf16 or fp32, rows out_stride elements apart
   uint16_t* xp;                     // workspace: x in the kernel's order, [chunks * NT][K]
   float* part;                      // workspace: two partial tiles a CTA
-  int32_t* count;                   // workspace: per tile, the CTAs that delivered their part
   WsHeader* ws;
   int64_t x_stride, out_stride;
   int M, N, K, group, out_f32;

@@ -22,8 +22,8 @@
 // SMs.  A unit is four 128 x 128 weight blocks: two row tiles of two
 // k blocks where there are many rows (x is then read once for 256 rows), or four k blocks of one
 // row tile (few rows).  Row tiles whose units lie on several
-// CTAs are summed from partials in the workspace by the CTA that arrives last, in the order of k,
-// so results do not depend on timing.
+// CTAs are summed from partials in the workspace by a second kernel, in the order of k, so results do
+// not depend on timing.
 #include <algorithm>
 
 #include "kernels.cuh"
@@ -40,7 +40,6 @@ struct W4Smem {
   uint64_t full[kWMaxStages], empty[kWMaxStages];
   uint64_t a_full[4], a_free[4], d_full[4], d_free[4], drain[2];
   uint32_t tmem;
-  int last;
 };
 
 // NT tokens a tile, KS k blocks a unit (of 4 / KS row tiles), GPB groups a k block of 128.
@@ -192,12 +191,11 @@ struct W4Row {
 }  // namespace
 
 // x [M][K] (rows x_stride apart) -> xp [rows][K], every eight values as 0 4 1 5 2 6 3 7 and rows
-// behind M zero; the tiles' arrival counters are cleared.
+// behind M zero.
 __global__ void __launch_bounds__(256) w4_prepare_kernel(W4Params p, int rows) {
   pdl_trigger();
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int c8 = p.K / 8;
-  for (int64_t t = i; t < p.tiles; t += (int64_t)gridDim.x * 256) p.count[t] = 0;
   if (i >= (int64_t)rows * c8) return;
   const int m = (int)(i / c8), c = (int)(i - (int64_t)m * c8);
   uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -224,14 +222,27 @@ __device__ __noinline__ void w4_scales(const W4Params& p, uint8_t* smem, W4Smem*
   for (int r = 0; r < 8; ++r)
 #pragma unroll
     for (int j = 0; j < Sh::kZWords; ++j) zp[r].w[j] = 0x08080808u;
-  auto fetch = [&](int rowt, int kb) {
+  const uint16_t* srow[8];
+  const uint8_t* zrow[8];
+  auto rows_of = [&](int rowt) {                        // once a segment
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
-      const int i = r * 32 + lane, wg = i >> 7;         // row i of the unit's 2 x 128
+      const int i = r * 32 + lane;                      // row i of the unit's 2 x 128
       const int n = min(rowt * Sh::kRows + (KS == 4 ? i & 127 : i), p.N - 1);
-      const int g = (kb * KS + (KS == 4 ? 2 * wg : 0)) * GPB;
-      sc[r].fetch(p.scales + (int64_t)n * ng, g, ng, wide);
-      if (p.zeros) zp[r].fetch(p.zeros + (int64_t)n * ng, g, ng, wide);
+      srow[r] = p.scales + (int64_t)n * ng;
+      zrow[r] = p.zeros + (int64_t)n * ng;
+    }
+  };
+  auto fetch = [&](int kb) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {              // rows of warpgroup 0, then of 1
+      const int g = (kb * KS + (KS == 4 ? 2 * half : 0)) * GPB;
+#pragma unroll
+      for (int r = 4 * half; r < 4 * half + 4; ++r) sc[r].fetch(srow[r], g, ng, wide);
+      if (p.zeros) {
+#pragma unroll
+        for (int r = 4 * half; r < 4 * half + 4; ++r) zp[r].fetch(zrow[r], g, ng, wide);
+      }
     }
   };
   W4Segment at;
@@ -240,7 +251,10 @@ __device__ __noinline__ void w4_scales(const W4Params& p, uint8_t* smem, W4Smem*
   int kb = at.kb, left = at.n, st = 0;
   uint32_t ph = 1;                                      // the first round of stages is free
   bool ok = true;
-  if (more) fetch(at.rowt, kb);
+  if (more) {
+    rows_of(at.rowt);
+    fetch(kb);
+  }
   while (more) {
     if (!mbar_wait(&sh->empty[st], ph)) { ok = false; break; }
     uint32_t* dst = reinterpret_cast<uint32_t*>(smem + st * Sh::kStage + Sh::kTx) + lane;
@@ -259,8 +273,9 @@ __device__ __noinline__ void w4_scales(const W4Params& p, uint8_t* smem, W4Smem*
       more = w4_segment(p, ++seg, at);
       kb = at.kb;
       left = at.n;
+      if (more) rows_of(at.rowt);
     }
-    if (more) fetch(at.rowt, kb);
+    if (more) fetch(kb);
   }
   if (!ok && lane == 0) report(p.ws, ETREE_ETIMEOUT, DET_WAIT_W4);
 }
@@ -341,7 +356,7 @@ __device__ __noinline__ void w4_sum(const W4Params& p, const uint8_t* smem, floa
                                     uint32_t tmem) {
   using Sh = W4Shape<NT, KS, GPB>;
   constexpr int kRows = Sh::kRows;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x - 12 * 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int wg = (warp - 12) >> 2, row = (warp & 3) * 32 + lane;
   const int wrow = (KS == 4 ? 0 : wg * 128) + row;
   const uint32_t ld = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256 + 128 * wg;
@@ -398,7 +413,7 @@ __device__ __noinline__ void w4_sum(const W4Params& p, const uint8_t* smem, floa
     int again = seg;                                    // the segment anew: it was not kept in
     asm volatile("" : "+r"(again));                     // registers beside the sums
     w4_segment(p, again, at);
-    const int rowt = at.rowt, tile = at.tile;
+    const int rowt = at.rowt;
     const int m0 = at.chunk * NT, mv = min(NT, p.M - m0);
     if constexpr (KS == 4) {                            // add the other warpgroup's sums
       if (wg == 1) {
@@ -443,7 +458,7 @@ __device__ __noinline__ void w4_sum(const W4Params& p, const uint8_t* smem, floa
         }
       }
     } else {
-      const int t0 = at.unit0 - at.kb, t1 = t0 + p.kbu;      // the tile's shared units
+      const int t0 = at.unit0 - at.kb;                  // the tile's first shared unit
       const int64_t part_size = (int64_t)NT * kRows;    // a CTA has room for two parts of tiles
       if (mine) {
         const int mine0 = w4_first(p, blockIdx.x);
@@ -451,56 +466,6 @@ __device__ __noinline__ void w4_sum(const W4Params& p, const uint8_t* smem, floa
 #pragma unroll
         for (int c = 0; c < NT; ++c)
           if (c < mv) dst[c * kRows] = half_of(acc[c / 2], c & 1);
-      }
-      __threadfence();
-      w4_sync();
-      const int c0 = w4_owner(p, t0);
-      const int c1 = w4_owner(p, t1 - 1);
-      if (tid == 0) sh->last = atomicAdd(p.count + tile, 1) == c1 - c0;
-      w4_sync();
-      if (sh->last) {
-        __threadfence();
-        // four rows of one token a thread, and four parts' loads of two tokens in flight at once
-        constexpr int step = 256 / (kRows / 4);
-        const int rr = tid % (kRows / 4) * 4, n = rowt * kRows + rr;
-        for (int m = tid / (kRows / 4); m < mv; m += 2 * step) {
-          float4 v[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-          for (int c = c0; c <= c1; c += 4) {
-            float4 x[4][2];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const bool first = w4_first(p, min(c + i, c1)) >= t0;
-              const float* src = p.part + (2 * min(c + i, c1) + (first ? 0 : 1)) * part_size + rr;
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                x[i][e] = c + i <= c1 && m + e * step < mv
-                              ? __ldcg(reinterpret_cast<const float4*>(src + (m + e * step) * kRows))
-                              : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                v[e].x += x[i][e].x;
-                v[e].y += x[i][e].y;
-                v[e].z += x[i][e].z;
-                v[e].w += x[i][e].w;
-              }
-          }
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            if (m + e * step >= mv) continue;
-            const float y[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
-            const int64_t o = (int64_t)(m0 + m + e * step) * p.out_stride + n;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (n + i < p.N) {
-                const float r = y[i] + bias_of(n + i);
-                if (p.out_f32) reinterpret_cast<float*>(p.out)[o + i] = r;
-                else reinterpret_cast<__nv_bfloat16*>(p.out)[o + i] = __float2bfloat16_rn(r);
-              }
-          }
-        }
       }
     }
     if constexpr (KS == 4) w4_sync();                   // `red` is free again
@@ -538,6 +503,7 @@ w4_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
     prefetch_tmap(&tm_q);
     prefetch_tmap(&tm_x);
   }
+  pdl_trigger();                                        // the join waits for this grid's end
   if (warp == 1) {
     tmem_alloc(&sh->tmem, 512);
     tmem_relinquish();
@@ -652,6 +618,43 @@ w4_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
   }
 }
 
+// Row tiles whose units lie on several CTAs: their parts are added in the order of k, four rows of
+// one token a thread.  One block row per shared tile.
+template <int NT, int KS>
+__global__ void __launch_bounds__(256) w4_join_kernel(const __grid_constant__ W4Params p) {
+  constexpr int kRows = 512 / KS, kQuads = kRows / 4;
+  pdl_wait();
+  pdl_trigger();
+  const int t0 = blockIdx.y * p.kbu;                    // the tile's first shared unit
+  const int c0 = w4_owner(p, t0), c1 = w4_owner(p, t0 + p.kbu - 1);
+  if (c0 == c1) return;                                 // one CTA's, already written
+  const int tile = p.tiles - p.share_units / p.kbu + blockIdx.y;
+  const int rowt = tile / p.chunks, m0 = (tile - rowt * p.chunks) * NT;
+  const int o = blockIdx.x * 256 + threadIdx.x, m = o / kQuads, rr = o % kQuads * 4;
+  const int n = rowt * kRows + rr;
+  if (m0 + m >= p.M || n >= p.N) return;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int c = c0; c <= c1; ++c) {
+    const bool first = w4_first(p, c) >= t0;
+    const float4 x = __ldcg(reinterpret_cast<const float4*>(
+        p.part + (2 * c + (first ? 0 : 1)) * ((int64_t)NT * kRows) + m * kRows + rr));
+    v.x += x.x;
+    v.y += x.y;
+    v.z += x.z;
+    v.w += x.w;
+  }
+  const float y[4] = {v.x, v.y, v.z, v.w};
+  const int64_t at = (int64_t)(m0 + m) * p.out_stride + n;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (n + i < p.N) {
+      const float r = y[i] + (p.bias ? __uint_as_float((uint32_t)__ldg(p.bias + n + i) << 16) : 0.f);
+      if (p.out_f32) reinterpret_cast<float*>(p.out)[at + i] = r;
+      else reinterpret_cast<__nv_bfloat16*>(p.out)[at + i] = __float2bfloat16_rn(r);
+    }
+}
+
 // Few tokens (at most 16): one launch, no tensor memory, no reordered x.  A warp takes MT x 16 rows
 // at every eighth k block and multiplies with mma.sync m16n8k16 (weights as A, NTL x 8 tokens as
 // B); the order of k inside a block is free as long as A and B agree, so a lane loads its rows'
@@ -681,6 +684,7 @@ struct W4SmallBlock {                                   // a lane's part of MT x
 template <int MT, int NTL, int GPB>
 __global__ void __launch_bounds__(32 * kSmallWarps) w4_small_kernel(const __grid_constant__ W4Params p) {
   constexpr int kRows = 16 * MT, kPart = NTL < 4 ? NTL : 4, kTok = 8 * kPart;
+  constexpr bool kAhead = NTL <= 2;
   __shared__ float sums[kSmallWarps][kTok][kRows + 1];  // kPart of the NTL token tiles at once
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int n0 = blockIdx.x * kRows, nkb = (p.K + 127) / 128, ng = p.K / p.group;
@@ -741,7 +745,19 @@ __global__ void __launch_bounds__(32 * kSmallWarps) w4_small_kernel(const __grid
   };
   float acc[MT][NTL][4] = {};
   const uint16_t* xrow = p.x + g * p.x_stride;          // token g, and every eighth after it
+  auto token = [&](int j, int k) {
+    return 8 * j + g < p.M && k < p.K
+               ? __ldg(reinterpret_cast<const uint4*>(xrow + 8 * j * p.x_stride + k))
+               : make_uint4(0u, 0u, 0u, 0u);
+  };
   auto multiply = [&](const W4SmallBlock<MT, GPB>& blk, int kb) {
+    uint4 xs[kAhead ? 4 : 1][NTL];                      // a block's tokens at once, if registers allow
+    if constexpr (kAhead) {
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+#pragma unroll
+        for (int j = 0; j < NTL; ++j) xs[w][j] = token(j, kb * 128 + first(w));
+    }
 #pragma unroll
     for (int gi = 0; gi < GPB; ++gi) {
       float d[MT][NTL][4] = {};
@@ -752,13 +768,11 @@ __global__ void __launch_bounds__(32 * kSmallWarps) w4_small_kernel(const __grid
         for (int h = 0; h < 2; ++h) zz[i][h] = (blk.z[i][h][gi] & 15u) * 0x00010001u | magic;
 #pragma unroll
       for (int w = gi * 4 / GPB; w < (gi + 1) * 4 / GPB; ++w) {
-        uint4 x[NTL];
-        const int k = kb * 128 + first(w);
+        uint4(&x)[NTL] = xs[kAhead ? w : 0];
+        if constexpr (!kAhead) {
 #pragma unroll
-        for (int j = 0; j < NTL; ++j)
-          x[j] = 8 * j + g < p.M && k < p.K
-                     ? __ldg(reinterpret_cast<const uint4*>(xrow + 8 * j * p.x_stride + k))
-                     : make_uint4(0u, 0u, 0u, 0u);
+          for (int j = 0; j < NTL; ++j) x[j] = token(j, kb * 128 + first(w));
+        }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {          // pairs (2 half, 2 half + 4), (.. + 1, .. + 5)
           uint32_t a[MT][4];
@@ -861,9 +875,12 @@ static cudaError_t go_w4(const CUtensorMap& q, const CUtensorMap& x, const W4Par
 template <int NT, int KS>
 static cudaError_t go_w4(const CUtensorMap& q, const CUtensorMap& x, const W4Params& p, int grid,
                          cudaStream_t s) {
-  if (p.group == 128) return go_w4<NT, KS, 1>(q, x, p, grid, s);
-  if (p.group == 64) return go_w4<NT, KS, 2>(q, x, p, grid, s);
-  return go_w4<NT, KS, 4>(q, x, p, grid, s);
+  cudaError_t e = p.group == 128  ? go_w4<NT, KS, 1>(q, x, p, grid, s)
+                  : p.group == 64 ? go_w4<NT, KS, 2>(q, x, p, grid, s)
+                                  : go_w4<NT, KS, 4>(q, x, p, grid, s);
+  if (e != cudaSuccess || p.share_units == 0) return e;
+  return launch_pdl(w4_join_kernel<NT, KS>, dim3(NT * (512 / KS) / 1024, p.share_units / p.kbu),
+                    dim3(256), 0, s, p);
 }
 
 cudaError_t launch_w4(const CUtensorMap& q, const CUtensorMap& x, const W4Params& p, int nt, int ks,
