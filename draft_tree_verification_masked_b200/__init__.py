@@ -198,7 +198,8 @@ def _ptr(t: torch.Tensor | None, dtype=None, name="tensor"):
 
 def _stream(stream) -> int | None:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # what torch.cuda.current_stream().cuda_stream gives, without its 3 us of wrapping
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -453,17 +454,27 @@ def etree_kv_compact(batch: Batch, accept_len, path, k_tree, v_tree, k_cache, v_
     return _check(st) if check else st
 
 
+def _arg(t, dtype, dev: int, n: int, name: str):
+    """Pointer of a contiguous tensor of `n` entries on device `dev` (None stays None).  The checks
+    of the serving calls: one short pass where all is well, since those calls take microseconds."""
+    if t is None:
+        return None
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.numel() == n and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor") from None
+    _ptr(t, dtype, name)                    # raises for the type, the host or the layout
+    _here(t)
+    raise ValueError(f"{name} must hold {n} entries, got {tuple(t.shape)}")
+
+
 def _here(*tensors):
     """Calls run on the current device's stream: tensors of another device are refused."""
     dev = torch.cuda.current_device()
     for t in tensors:
         if t is not None and t.is_cuda and t.device.index != dev:
             raise ValueError(f"a tensor lives on {t.device}, the current device is cuda:{dev}")
-
-
-def _numel(t, n: int, name: str):
-    if t is not None and t.numel() != n:
-        raise ValueError(f"{name} must hold {n} entries, got {tuple(t.shape)}")
 
 
 def etree_page_plan(cu_new, kv_len, page_size: int, num_pages: int, pages_held, free_ring,
@@ -473,58 +484,61 @@ def etree_page_plan(cu_new, kv_len, page_size: int, num_pages: int, pages_held, 
     pages_held int32 [B], free_ring int32 [num_pages], ring_state int64 [2], block_table int32
     [B, max_pages] (updated in place); slot_cap int32 [B] and slot_map int64 may be None."""
     i32, i64 = torch.int32, torch.int64
-    B = kv_len.numel()
-    for t, n, name in ((cu_new, B + 1, "cu_new"), (pages_held, B, "pages_held"),
-                       (free_ring, int(num_pages), "free_ring"), (ring_state, 2, "ring_state"),
-                       (pages_held_out, B, "pages_held_out"),
-                       (ring_state_out, 2, "ring_state_out"), (slot_cap, B, "slot_cap"),
-                       (block_table, B * block_table.shape[-1], "block_table")):
-        _numel(t, n, name)
-    args = (
-        B, 0 if slot_map is None else slot_map.numel(), _ptr(cu_new, i32, "cu_new"),
-        _ptr(kv_len, i32, "kv_len"), int(page_size), block_table.shape[-1], int(num_pages),
-        _ptr(pages_held, i32, "pages_held"), _ptr(free_ring, i32, "free_ring"),
-        _ptr(ring_state, i64, "ring_state"), _ptr(block_table, i32, "block_table"),
-        _ptr(pages_held_out, i32, "pages_held_out"), _ptr(ring_state_out, i64, "ring_state_out"),
-        _ptr(slot_cap, i32, "slot_cap"), _ptr(slot_map, i64, "slot_map"),
-        _ptr(workspace, torch.uint8, "workspace"), workspace.numel())
-    _here(cu_new, kv_len, pages_held, free_ring, ring_state, block_table, pages_held_out,
-          ring_state_out, slot_cap, slot_map, workspace)
-    st = lib().etree_page_plan(*args, _stream(stream))
+    B, max_pages, dev = kv_len.numel(), block_table.shape[-1], torch.cuda.current_device()
+    page_size, num_pages = int(page_size), int(num_pages)
+    tokens = 0 if slot_map is None else slot_map.numel()
+    st = lib().etree_page_plan(
+        B, tokens, _arg(cu_new, i32, dev, B + 1, "cu_new"), _arg(kv_len, i32, dev, B, "kv_len"),
+        page_size, max_pages, num_pages, _arg(pages_held, i32, dev, B, "pages_held"),
+        _arg(free_ring, i32, dev, num_pages, "free_ring"),
+        _arg(ring_state, i64, dev, 2, "ring_state"),
+        _arg(block_table, i32, dev, B * max_pages, "block_table"),
+        _arg(pages_held_out, i32, dev, B, "pages_held_out"),
+        _arg(ring_state_out, i64, dev, 2, "ring_state_out"), _arg(slot_cap, i32, dev, B, "slot_cap"),
+        _arg(slot_map, i64, dev, tokens, "slot_map"), *_work(workspace, dev), _stream(stream))
     return _check(st) if check else st
 
 
-def _rows(t, name: str):
+def _work(workspace, dev: int):
+    """Pointer and size of a workspace."""
+    n = workspace.numel()
+    return _arg(workspace, torch.uint8, dev, n, "workspace"), n
+
+
+def _rows(t, name: str, dev: int):
     """Pointer and row stride of a [rows, heads, dims] bf16 tensor whose rows are dense inside."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
+    _, h, d = t.shape
+    s0, s1, s2 = t.stride()
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.get_device() != dev:
+        _on_device(t, name)
+    if (d > 1 and s2 != 1) or (h > 1 and s1 != d):
+        raise ValueError(f"{name}: a row's heads must be contiguous")
+    return t.data_ptr(), (s0 if t.shape[0] > 1 else h * d)
+
+
+def _on_device(t, name: str):
     if not t.is_cuda:
         raise ValueError(f"{name} must live on a CUDA device")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    n, h, d = t.shape
-    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
-        raise ValueError(f"{name}: a row's heads must be contiguous")
-    return t.data_ptr(), (t.stride(0) if n > 1 else h * d)
+    _here(t)
 
 
 def etree_kv_store(slot_map, k, v, k_pool, v_pool, workspace, stream=None,
                    check: bool = True) -> int:
     """slot_map int64 [n]; k, v bf16 [n, hkv, 128], rows any stride apart (views of a fused
     projection, say); pools bf16 [slots, hkv, 128]."""
-    bf = torch.bfloat16
+    bf, dev = torch.bfloat16, torch.cuda.current_device()
     n, hkv, d = k.shape
-    if tuple(v.shape) != (n, hkv, d) or tuple(k_pool.shape[1:]) != (hkv, d) or \
-            k_pool.shape != v_pool.shape:
+    slots = k_pool.shape[0]
+    if v.shape != k.shape or k_pool.shape != (slots, hkv, d) or v_pool.shape != k_pool.shape:
         raise ValueError("k, v and the pools must have the same heads")
-    _numel(slot_map, n, "slot_map")
-    kp, ks = _rows(k, "k")
-    vp, vs = _rows(v, "v")
-    args = (_ptr(slot_map, torch.int64, "slot_map"), n, kp, ks, vp, vs,
-            _ptr(k_pool, bf, "k_pool"), _ptr(v_pool, bf, "v_pool"), k_pool.shape[0], hkv, d,
-            _ptr(workspace, torch.uint8, "workspace"), workspace.numel())
-    _here(slot_map, k, v, k_pool, v_pool, workspace)
-    st = lib().etree_kv_store(*args, _stream(stream))
+    (kp, ks), (vp, vs) = _rows(k, "k", dev), _rows(v, "v", dev)
+    size = slots * hkv * d
+    st = lib().etree_kv_store(
+        _arg(slot_map, torch.int64, dev, n, "slot_map"), n, kp, ks, vp, vs,
+        _arg(k_pool, bf, dev, size, "k_pool"), _arg(v_pool, bf, dev, size, "v_pool"), slots, hkv, d,
+        *_work(workspace, dev), _stream(stream))
     return _check(st) if check else st
 
 
@@ -535,24 +549,22 @@ def etree_attn_diff_workspace_size(batch: Batch, hq: int, hkv: int) -> int:
 def _diff_args(batch, q, k_tree, v_tree, k_cache, v_cache, slots, scale, lam, norm_w, norm_eps,
                out_scale, out, lse, workspace):
     """The arguments that the contiguous and the paged call share, checked."""
-    bf, f32 = torch.bfloat16, torch.float32
+    bf, f32, dev = torch.bfloat16, torch.float32, torch.cuda.current_device()
     n, hq, d = q.shape
     hkv = k_tree.shape[1]
-    if n != batch.n_total or tuple(k_tree.shape) != (n, hkv, d) or v_tree.shape != k_tree.shape:
+    if n != batch.n_total or k_tree.shape != (n, hkv, d) or v_tree.shape != k_tree.shape:
         raise ValueError(f"q, k_tree and v_tree must hold {batch.n_total} nodes of {d} dims")
-    if tuple(k_cache.shape[1:]) != (hkv, d) or k_cache.shape != v_cache.shape:
+    if k_cache.shape[1:] != (hkv, d) or k_cache.shape != v_cache.shape:
         raise ValueError("the caches must have k_tree's heads")
     if out.shape != q.shape:
         raise ValueError("out must have q's shape")
-    _numel(lam, hq, "lam")
-    _numel(norm_w, d, "norm_w")
-    _numel(lse, n * hq * 2, "lse")
-    (qp, qs), (kp, ks), (vp, vs) = _rows(q, "q"), _rows(k_tree, "k_tree"), _rows(v_tree, "v_tree")
-    _here(q, k_tree, v_tree, k_cache, v_cache, lam, norm_w, out, lse, workspace)
-    return (qp, qs, kp, ks, vp, vs, _ptr(k_cache, bf, "k_cache"), _ptr(v_cache, bf, "v_cache"),
-            slots, hq, hkv, d, float(scale), _ptr(lam, f32, "lam"), _ptr(norm_w, bf, "norm_w"),
-            float(norm_eps), float(out_scale), _ptr(out, bf, "out"), _ptr(lse, f32, "lse"),
-            _ptr(workspace, torch.uint8, "workspace"), workspace.numel())
+    size = k_cache.shape[0] * hkv * d
+    return (*_rows(q, "q", dev), *_rows(k_tree, "k_tree", dev), *_rows(v_tree, "v_tree", dev),
+            _arg(k_cache, bf, dev, size, "k_cache"), _arg(v_cache, bf, dev, size, "v_cache"), slots,
+            hq, hkv, d, float(scale), _arg(lam, f32, dev, hq, "lam"),
+            _arg(norm_w, bf, dev, d, "norm_w"), float(norm_eps), float(out_scale),
+            _arg(out, bf, dev, n * hq * d, "out"), _arg(lse, f32, dev, n * hq * 2, "lse"),
+            *_work(workspace, dev))
 
 
 def etree_verify_attn_diff(batch: Batch, q, k_tree, v_tree, k_cache, v_cache, scale: float, lam,
@@ -572,12 +584,10 @@ def etree_verify_attn_diff_paged(batch: Batch, block_table, page_size: int, q, k
                                  out_scale: float, out, lse, workspace, stream=None,
                                  check: bool = True) -> int:
     """The same over pools [num_pages * page_size, hkv, 128]; block_table int32 [B, max_pages]."""
-    if block_table.numel() != batch.B * block_table.shape[-1]:
-        raise ValueError(f"block_table must have {batch.B} rows")
-    _here(block_table)
+    max_pages, dev = block_table.shape[-1], torch.cuda.current_device()
     st = lib().etree_verify_attn_diff_paged(
-        C.byref(batch), _ptr(block_table, torch.int32, "block_table"), block_table.shape[-1],
-        int(page_size), *_diff_args(batch, q, k_tree, v_tree, k_pool, v_pool,
+        C.byref(batch), _arg(block_table, torch.int32, dev, batch.B * max_pages, "block_table"),
+        max_pages, int(page_size), *_diff_args(batch, q, k_tree, v_tree, k_pool, v_pool,
                                     k_pool.shape[0] // max(1, int(page_size)), scale, lam, norm_w,
                                     norm_eps, out_scale, out, lse, workspace),
         _stream(stream))
@@ -593,40 +603,37 @@ def etree_w4_linear(x, wq, scales, zeros, group: int, bias, out, workspace, stre
     """x bf16 [M, K]; wq uint8 [N, K / 2], two weights a byte; scales bf16 [N, K / group]; zeros
     uint8 [N, K / group] or None; bias bf16 [N] or None; out bf16 or fp32 [M, N].  Rows of x and
     out may lie any stride apart."""
-    bf, u8 = torch.bfloat16, torch.uint8
+    bf, u8, dev = torch.bfloat16, torch.uint8, torch.cuda.current_device()
     M, K = x.shape
-    N = wq.shape[0]
-    group = int(group)
-    if out.dtype not in (bf, torch.float32):
+    N, group = wq.shape[0], int(group)
+    f32 = out.dtype is torch.float32
+    if not f32 and out.dtype is not bf:
         raise TypeError(f"out must be bfloat16 or float32, got {out.dtype}")
-    if tuple(wq.shape) != (N, K // 2) or tuple(out.shape) != (M, N):
+    if wq.shape != (N, K // 2) or out.shape != (M, N):
         raise ValueError(f"wq and out must be [N, {K // 2}] and [{M}, N]")
-    groups = (N, K // max(1, group))
-    if tuple(scales.shape) != groups or (zeros is not None and tuple(zeros.shape) != groups):
-        raise ValueError(f"scales and zeros must be {groups}")
-    _numel(bias, N, "bias")
-    xp, xs = _matrix(x, bf, "x")
-    op, os_ = _matrix(out, out.dtype, "out")
-    _here(x, wq, scales, zeros, bias, out, workspace)
+    groups = K // max(1, group)
+    if scales.shape != (N, groups) or (zeros is not None and zeros.shape != (N, groups)):
+        raise ValueError(f"scales and zeros must be {(N, groups)}")
+    (xp, xs), (op, os_) = _matrix(x, bf, "x", dev), _matrix(out, out.dtype, "out", dev)
     st = lib().etree_w4_linear(
-        xp, xs, M, _ptr(wq, u8, "wq"), _ptr(scales, bf, "scales"), _ptr(zeros, u8, "zeros"), group,
-        N, K, _ptr(bias, bf, "bias"), op, os_, int(out.dtype == torch.float32),
-        _ptr(workspace, u8, "workspace"), workspace.numel(), _stream(stream))
+        xp, xs, M, _arg(wq, u8, dev, N * (K // 2), "wq"),
+        _arg(scales, bf, dev, N * groups, "scales"), _arg(zeros, u8, dev, N * groups, "zeros"),
+        group, N, K, _arg(bias, bf, dev, N, "bias"), op, os_, int(f32), *_work(workspace, dev),
+        _stream(stream))
     return _check(st) if check else st
 
 
-def _matrix(t, dtype, name: str):
+def _matrix(t, dtype, name: str, dev: int):
     """Pointer and row stride of a [rows, columns] tensor whose rows are dense inside."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must live on a CUDA device")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        _on_device(t, name)
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    s0, s1 = t.stride()
+    if cols > 1 and s1 != 1:
         raise ValueError(f"{name}: rows must be contiguous")
-    return t.data_ptr(), (t.stride(0) if rows > 1 else cols)
+    return t.data_ptr(), (s0 if rows > 1 else cols)
 
 
 def etree_attn_plan(batch: Batch, hq: int, hkv: int) -> dict:

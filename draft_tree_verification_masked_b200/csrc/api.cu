@@ -815,7 +815,8 @@ static etree_status attn_diff_impl(const etree_batch* b, const uint16_t* q, int6
   p.cache_box = (int)cbox;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (b->B >= 8) {                             // mixed lengths: the longest requests start first
+  // mixed lengths and more CTAs than SMs: the longest requests start first
+  if (b->B >= 8 && (int64_t)b->B * hkv * pl.mchunks * pl.nsplit > sm_count()) {
     int32_t* order = at<int32_t>(workspace, w.order);
     p.order = order;
     e = launch_attn_order(b->kv_len, b->B, order, s);
@@ -951,7 +952,10 @@ etree_status etree_w4_linear(const uint16_t* x, int64_t x_stride, int M, const u
   p.group = group;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (w4_is_small(M, N, K)) {
-    const cudaError_t e = launch_w4_small(p, N >= 64 * sm_count() ? 2 : 1, s);
+    // two row tiles a warp read x half as often; taken where all SMs still get a CTA (8 tokens of
+    // 7168 x 5120: 8.9 us against 11.9), and two with more tokens (32 of 4800 x 5120: 20.9 against 17.8)
+    const int mt = N >= (M <= 16 ? 32 : 64) * sm_count() ? 2 : 1;
+    const cudaError_t e = launch_w4_small(p, mt, s);
     return e == cudaSuccess ? ETREE_OK : cuda_fail(e, "etree_w4_linear launch");
   }
   CUtensorMap tq, tx;

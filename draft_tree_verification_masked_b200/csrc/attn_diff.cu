@@ -642,8 +642,7 @@ cudaError_t launch_attn_diff(const CUtensorMap& q, const CUtensorMap& kc, const 
                              const CUtensorMap& kt, const CUtensorMap& vt, const DiffParams& p,
                              cudaStream_t stream) {
   const size_t smem = 1024 + kDQ + (size_t)kDStages * kDKV + sizeof(DiffSmem);
-  cudaError_t e = cudaFuncSetAttribute(attn_diff_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = raise_smem_once(attn_diff_kernel, (int)smem);
   if (e != cudaSuccess) return e;
   dim3 grid(p.B * p.hkv * p.mchunks, p.nsplit);
   attn_diff_kernel<<<grid, kDThreads, smem, stream>>>(q, kc, vc, kt, vt, p);

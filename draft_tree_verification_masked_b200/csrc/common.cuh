@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <mutex>
 #include <utility>
 
 #include "etree.h"
@@ -374,6 +375,28 @@ __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;"
 
 __device__ __forceinline__ void pdl_trigger() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Raises a kernel's dynamic shared memory limit to `bytes`, the one size it is launched with: once
+// per device (the attribute belongs to the device's context and stays).
+template <typename... KArgs>
+static cudaError_t raise_smem_once(void (*kernel)(KArgs...), int bytes) {
+  static std::mutex mu;
+  static struct { const void* kernel; int dev; } done[64];
+  static int count = 0;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const void* k = reinterpret_cast<const void*>(kernel);
+  std::lock_guard<std::mutex> lk(mu);
+  for (int i = 0; i < count; ++i)
+    if (done[i].kernel == k && done[i].dev == dev) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && count < 64) {                 // past that, it is set at every call
+    done[count].kernel = k;
+    done[count++].dev = dev;
+  }
+  return e;
 }
 
 template <typename... KArgs, typename... Args>

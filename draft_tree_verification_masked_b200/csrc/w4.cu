@@ -866,8 +866,7 @@ cudaError_t launch_w4_small(const W4Params& p, int mt, cudaStream_t s) {
 template <int NT, int KS, int GPB>
 static cudaError_t go_w4(const CUtensorMap& q, const CUtensorMap& x, const W4Params& p, int grid,
                          cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(w4_kernel<NT, KS, GPB>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kWSmem);
+  const cudaError_t e = raise_smem_once(w4_kernel<NT, KS, GPB>, kWSmem);
   if (e != cudaSuccess) return e;
   return launch_pdl(w4_kernel<NT, KS, GPB>, dim3(grid), dim3(kWThreads), (size_t)kWSmem, s, q, x, p);
 }
