@@ -16,16 +16,24 @@
 //   O_m += P_m V       tcgen05.mma M=128 x N=128 x K=64, P_m (bf16) read from TMEM.
 //
 // One CTA = (request, KV head, 128-row block, KV split); row = node * G + g.  Warp 0 streams Q and
-// the K/V ring, warp 1 issues the MMAs, and each map has four softmax warps (one row per thread,
-// one TMEM lane).  TMEM holds both O accumulators (256 columns), one S buffer per map (128) and two
-// P buffers per map (128): all 512 columns, so one CTA runs per SM.  One S buffer is enough because
-// the softmax copies it to registers at once; the next tile's S_m is computed while it works on
-// this one's exponentials.  Those are the second bound after HBM: two maps x 128 rows x 64 keys at
-// 16 a clock take 1024 clocks a tile, against about 1400 for the tile's 32 KB at an SM's share of
-// HBM; warps without a row of the tree skip them.
+// the K/V ring; each map has an MMA warp and four softmax warps (one row per thread, one TMEM
+// lane).  TMEM holds both O accumulators (256 columns) and two buffers of 64 columns a map, in which
+// P replaces the S that it was made from: all 512 columns, so one CTA runs per SM.  S of tile j + 2
+// is issued once the product with P of tile j has left its buffer, so S of the next tile is always
+// there when the softmax asks for it.
+//
+// Floor of 64 ragged requests (16 nodes, 40 query heads, 8 KV heads, 1K to 8K cached): 1.23 GB of
+// cache, 190 us at the copy rate.  Measured 276 us, 4.4 TB/s; 128K cached tokens of one request
+// 123-143 us (floor 83); one request with 64 nodes over 4K 31 us (floor 5).  What bounds it is the
+// softmax of a tile: about 1 us from one S to the next, of which the exponentials, two maps x 64
+// keys a row at 16 a clock and SM, are half.  Measured on the ragged batch and not kept:
+// sixteen softmax warps with 32 keys each 291 us, the two maps' exponentials taking turns 287 us,
+// half of the exponentials as polynomials on the FMA units 331 us (against 276 us each).
 //
 // P is rounded to bf16, the operand type of V; the row sums add the unrounded fp32 values, and
-// maxima, sums and both outputs stay in fp32 until the one rounding of `out`.  O is rescaled only
+// maxima, sums and both outputs stay in fp32 until the one rounding of `out`.  (P as the sum of two
+// bf16 operands removes that rounding and costs 370 to 400 us on the ragged batch; the rounding adds
+// about as much to an output's error as the output's own rounding to bf16 does.)  O is rescaled only
 // when a row's maximum grows by more than 2^8.
 //
 // A key that no row may see takes no part: V rows behind the last cached key and behind the last
