@@ -530,7 +530,8 @@ w4_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
         for (int w = 0; w < 2 * KS; ++w)
           tma_load_2d(dst + w * (NT * 128), &tm_x, &sh->full[st], kb * KS * 128 + w * 64, chunk * NT);
       };
-      // the first weights do not depend on the kernel that reorders x
+      // the first weights do not depend on the kernel that reorders x (an ordinary launch, before
+      // which everything earlier on the stream has completed)
       int ahead = 0;
       W4Segment at;
       for (int seg = 0; ahead < kStages && w4_segment(p, seg, at); ++seg)
@@ -655,7 +656,7 @@ __global__ void __launch_bounds__(256) w4_join_kernel(const __grid_constant__ W4
     }
 }
 
-// Few tokens (at most 16): one launch, no tensor memory, no reordered x.  A warp takes MT x 16 rows
+// Few tokens or small products: one launch, no tensor memory, no reordered x.  A warp takes MT x 16 rows
 // at every eighth k block and multiplies with mma.sync m16n8k16 (weights as A, NTL x 8 tokens as
 // B); the order of k inside a block is free as long as A and B agree, so a lane loads its rows'
 // bytes and its token's values in runs, in words of eight weights whose k lie in one group:
@@ -810,10 +811,10 @@ __global__ void __launch_bounds__(32 * kSmallWarps) w4_small_kernel(const __grid
     }
   };
   W4SmallBlock<MT, GPB> even, odd;
-  int kb = warp;
-  if (kb < nkb) load(even, kb);                         // weights do not depend on earlier kernels
-  pdl_wait();
+  pdl_wait();                                           // the weights too may be fresh
   pdl_trigger();
+  int kb = warp;
+  if (kb < nkb) load(even, kb);
   while (kb < nkb) {
     if (kb + kSmallWarps < nkb) load(odd, kb + kSmallWarps);
     multiply(even, kb);
