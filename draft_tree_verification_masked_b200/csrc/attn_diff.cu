@@ -13,28 +13,27 @@
 //
 //   S_m  = Q_m K_m^T   tcgen05.mma M=128 (rows) x N=64 (keys) x K=64, the two 64-dim boxes of Q and
 //                      K that the TMA loads bring anyway;
-//   O_m += P_m V       tcgen05.mma M=128 x N=128 x K=64, P_m (bf16) read from TMEM.
+//   O_m += P_m V       tcgen05.mma M=128 x N=128 x K=64 for each part of P_m (bf16, from TMEM).
 //
 // One CTA = (request, KV head, 128-row block, KV split); row = node * G + g.  Warp 0 streams Q and
 // the K/V ring; each map has an MMA warp and four softmax warps (one row per thread, one TMEM
 // lane).  TMEM holds both O accumulators (256 columns) and two buffers of 64 columns a map, in which
-// P replaces the S that it was made from: all 512 columns, so one CTA runs per SM.  S of tile j + 2
-// is issued once the product with P of tile j has left its buffer, so S of the next tile is always
-// there when the softmax asks for it.
+// P's two parts replace the S that they were made from: all 512 columns, so one CTA runs per SM.
+// S of tile j + 2 is issued once the products with P of tile j have left its buffer, so S of the
+// next tile is always there when the softmax asks for it.
+//
+// P enters the product with V as the sum of two bf16 operands, off by at most 2^-14 of each value:
+// rounding P to one bf16 would add as much to an output's error as its own rounding to bf16 does.
+// The row sums add the unrounded fp32 values, and maxima, sums and both outputs stay in fp32 until
+// the one rounding of `out`.  O is rescaled only when a row's maximum grows by more than 2^8.
 //
 // Floor of 64 ragged requests (16 nodes, 40 query heads, 8 KV heads, 1K to 8K cached): 1.23 GB of
-// cache, 190 us at the copy rate.  Measured 276 us, 4.4 TB/s; 128K cached tokens of one request
-// 123-143 us (floor 83); one request with 64 nodes over 4K 31 us (floor 5).  What bounds it is the
-// softmax of a tile: about 1 us from one S to the next, of which the exponentials, two maps x 64
-// keys a row at 16 a clock and SM, are half.  Measured on the ragged batch and not kept:
-// sixteen softmax warps with 32 keys each 291 us, the two maps' exponentials taking turns 287 us,
-// half of the exponentials as polynomials on the FMA units 331 us (against 276 us each).
-//
-// P is rounded to bf16, the operand type of V; the row sums add the unrounded fp32 values, and
-// maxima, sums and both outputs stay in fp32 until the one rounding of `out`.  (P as the sum of two
-// bf16 operands removes that rounding and costs 370 to 400 us on the ragged batch; the rounding adds
-// about as much to an output's error as the output's own rounding to bf16 does.)  O is rescaled only
-// when a row's maximum grows by more than 2^8.
+// cache, 190 us at the copy rate.  Measured 331 us, 3.7 TB/s (274 us with P rounded to one bf16);
+// 128K cached tokens of one request 158 us (floor 83; 125-130); one request with 64 nodes over 4K
+// 32 us (floor 5; 30).  What bounds it is the softmax of a tile, instruction by instruction: about
+// 1 us from one S to the next.  Measured on the ragged batch with one bf16 P and not kept: sixteen
+// softmax warps with 32 keys each 291 us, the two maps' exponentials taking turns 287 us, half of
+// the exponentials as polynomials on the FMA units 331 us.
 //
 // A key that no row may see takes no part: V rows behind the last cached key and behind the last
 // tree node are zeroed in shared memory (0 x NaN would be NaN), and a tree node's infinite or NaN
@@ -51,7 +50,8 @@ constexpr int kDBox = kDKeys * 128;         // one [64 keys][64 dims] bf16 box
 constexpr int kDKV = 4 * kDBox;             // K halves, V halves
 constexpr int kDQ = 2 * 16384;              // Q halves, [128 rows][64 dims]
 constexpr float kDLazy = 8.0f;              // rescale O only when the maximum grows by > 2^8
-// TMEM columns: O_m at 128 m; buffer b of map m at 256 + 128 m + 64 b: S (fp32), then P in its place
+// TMEM columns: O_m at 128 m; buffer b of map m at 256 + 128 m + 64 b: S (fp32), then P's
+// parts (32 columns each) in its place
 constexpr int kDS = 256, kDCols = 512;
 constexpr int kDThreads = 32 * 12;
 
@@ -86,11 +86,16 @@ __device__ __forceinline__ float diff2(float a, float w0, float b, float w1) {
   return __fadd_rn(__fmul_rn(a, w0), __fmul_rn(b, w1));
 }
 
-// Two fp32 words as a pair of bf16, rounded to the nearest with ties away from zero (finite values
-// and infinities; a NaN becomes a number, so its row's sum has to carry it).  Three integer
-// operations: the conversion instruction runs at the exponentials' rate and beside them.
-__device__ __forceinline__ uint32_t round_pair(uint32_t lo, uint32_t hi) {
-  return __byte_perm(lo + 0x8000u, hi + 0x8000u, 0x7632);
+// A pair of non-negative fp32 values as two pairs of bf16 whose sum is off by at most 2^-14 of the
+// value: the upper halves of the words, and what they leave, cut to bf16 as well.
+__device__ __forceinline__ uint32_t upper_pair(float a, float b) {
+  return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+}
+__device__ __forceinline__ uint32_t lower_pair(float a, float b) {
+  float r0 = __uint_as_float((__float_as_uint(a) & 0xffff0000u) | 0x80000000u);   // minus the upper half
+  float r1 = __uint_as_float((__float_as_uint(b) & 0xffff0000u) | 0x80000000u);
+  fadd2(r0, r1, a, b);
+  return upper_pair(r0, r1);
 }
 
 // 64 consecutive fp32 columns of this thread's TMEM lane, in one load.
@@ -117,6 +122,16 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
   for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Writes 16 consecutive 32-bit columns of this thread's TMEM lane without waiting for them.
+__device__ __forceinline__ void tmem_st16_async(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
 }
 
 __device__ __forceinline__ void softmax_warps_sync() {
@@ -344,6 +359,9 @@ attn_diff_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         for (int k = 0; k < kDKeys / 16; ++k)
           tc_mma_bf16_ts(tmem + 128 * m, pa + 8 * k, dv + k * (2048 >> 4), idO,
                          (j > 0 || k > 0) ? 1u : 0u);
+#pragma unroll
+        for (int k = 0; k < kDKeys / 16; ++k)           // what the first part left
+          tc_mma_bf16_ts(tmem + 128 * m, pa + 32 + 8 * k, dv + k * (2048 >> 4), idO, 1u);
         tc_commit(&sh->o_done[m]);
         tc_commit(&sh->kv_empty[vs]);
       }
@@ -434,20 +452,26 @@ attn_diff_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const float m_new = need ? tms : m_ref;
         const float off = m_new == -INFINITY ? 0.f : m_new;
         float a0 = 0.f, a1 = 0.f;
-        float pk[32];                                   // bf16 pairs, as the 32-bit columns of P
 #pragma unroll
-        for (int c = 0; c < 32; c += 2) {
-          float x0, x1, x2, x3;
-          ffma2(x0, x1, sc[2 * c], sc[2 * c + 1], sl, -off);
-          ffma2(x2, x3, sc[2 * c + 2], sc[2 * c + 3], sl, -off);
-          const float e0 = ex2_approx(x0), e1 = ex2_approx(x1);
-          const float e2 = ex2_approx(x2), e3 = ex2_approx(x3);
-          fadd2(a0, a1, e0, e1);
-          fadd2(a0, a1, e2, e3);
-          const uint32_t u[4] = {__float_as_uint(e0), __float_as_uint(e1), __float_as_uint(e2),
-                                 __float_as_uint(e3)};
-          pk[c] = __uint_as_float(round_pair(u[0], u[1]));
-          pk[c + 1] = __uint_as_float(round_pair(u[2], u[3]));
+        for (int half = 0; half < 2; ++half) {          // 32 keys: 16 columns of bf16 pairs
+          uint32_t hi[16], lo[16];                      // P's first part, and what it leaves
+#pragma unroll
+          for (int c = 0; c < 16; c += 2) {
+            const float* z = sc + 32 * half + 2 * c;
+            float x0, x1, x2, x3;
+            ffma2(x0, x1, z[0], z[1], sl, -off);
+            ffma2(x2, x3, z[2], z[3], sl, -off);
+            const float e0 = ex2_approx(x0), e1 = ex2_approx(x1);
+            const float e2 = ex2_approx(x2), e3 = ex2_approx(x3);
+            fadd2(a0, a1, e0, e1);
+            fadd2(a0, a1, e2, e3);
+            hi[c] = upper_pair(e0, e1);
+            hi[c + 1] = upper_pair(e2, e3);
+            lo[c] = lower_pair(e0, e1);
+            lo[c + 1] = lower_pair(e2, e3);
+          }
+          tmem_st16_async(buf + 16 * half, hi);
+          tmem_st16_async(buf + 32 + 16 * half, lo);
         }
         const float corr = need ? ex2_approx(m_ref - m_new) : 1.f;
         l = l * corr + (a0 + a1);
@@ -466,7 +490,7 @@ attn_diff_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             tmem_st32(ta, o);
           }
         }
-        tmem_st32(buf, pk);
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_fence_before();
       }
       __syncwarp();

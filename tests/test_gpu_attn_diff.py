@@ -1,16 +1,12 @@
 """Differential tree attention on the GPU against its fp64 definition.
 
-Tolerances.  The kernel rounds each probability to bf16 (a relative error of at most 2^-8) and the
-output once (2^-8 of its value).  Scores are fp32 sums of 64 exact products, off by at most
+Tolerances.  Each probability enters its product with V as two bf16 parts, the upper half of the
+fp32 word and the upper half of what that leaves, off by less than 2^-14 of it together; the output
+is rounded once (2^-8 of its value).  Scores are fp32 sums of 64 exact products, off by at most
 g = 66 * 2^-24 times scale * sum |q k| (at most `Z` over a case's keys), which moves a probability
 and the sum it is divided by by a factor within exp(2 g Z); exponentials, sums and divisions in
-fp32 stay within 2^-18 together.  So with e = 2^-8 + 2 g Z + 2^-18,
+fp32 stay within 2^-18 together.  So with e = 2^-14 + 2 g Z + 2^-18,
   |d - exact| <= e (a_1 |V| + lambda a_2 |V|) =: t.
-Over a long cache that bound of the bf16 roundings is as large as d itself, which shrinks with the
-number of keys.  There they are held to a tighter one: a rounding to the nearest is an error of at
-most c_i = 2^-8 p_i |v_i| of either sign, unrelated from key to key, and the sum of such errors is
-above 7 sqrt(sum c_i^2) with a chance of at most 2 exp(-49 / 2) = 5e-11 (Hoeffding).  t takes the
-smaller of both for the roundings' part.
 With t, the norm, whose factor f = 1 / sqrt(mean d^2 + eps) moves by at most |t| / |d| (2-norms over the
 head, times 1.2 while that ratio is below 1/8), carries it to f (t + 1.2 |d| |t| / |d|_2).
 """
@@ -126,12 +122,7 @@ class Case:
             keys = np.concatenate([f[3][self.rows[r]], f[1][a:b]])
             Z = max((np.abs(f[0][a:b, h]) @ np.abs(keys[:, h // G]).T).max()
                     for h in range(self.hq)) * self.scale
-            sq = [S.attention_diff(*one[:5], f[2][a:b] ** 2, f[3], f[4] ** 2, 2 * self.scale,
-                                   np.full(self.hq, x)) for x in (0.0, -1.0)]
-            p2 = np.exp(sq[0][1] - 2 * lse)[..., None]          # sum p^2, by which p^2 is scaled
-            var = p2[:, :, 0] * sq[0][0] + lam[:, None] ** 2 * p2[:, :, 1] * (sq[1][0] - sq[0][0])
-            tol = np.minimum(2.0 ** -8 * mass, 7 * 2.0 ** -8 * np.sqrt(np.maximum(var, 0)))
-            tol = tol + (2 * G_SCORE * Z + 2.0 ** -18) * mass
+            tol = (2.0 ** -14 + 2 * G_SCORE * Z + 2.0 ** -18) * mass
             if w is not None:
                 fac = 1 / np.sqrt((d * d).mean(-1, keepdims=True) + self.eps)
                 rel = np.linalg.norm(tol, axis=-1, keepdims=True) / np.linalg.norm(

@@ -138,7 +138,7 @@ def test_prompts_then_tree_steps():
                                    -lam.double().cpu().numpy())
         keys = np.nanmax(np.abs(np.concatenate([f[1], f[3]])))
         Z = 0.125 * np.abs(f[0]).sum(-1).max() * keys
-        tol = (2.0 ** -8 + 2 * 66 * 2.0 ** -24 * Z + 2.0 ** -18) * mass + 2.0 ** -8 * np.abs(want)
+        tol = (2.0 ** -14 + 2 * 66 * 2.0 ** -24 * Z + 2.0 ** -18) * mass + 2.0 ** -8 * np.abs(want)
         assert (np.abs(out.double().cpu().numpy() - want) <= tol + 1e-30).all()
         y = torch.empty(nt, H, dtype=bf, device="cuda")
         w_out(out.flatten(1), y)
