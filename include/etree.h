@@ -190,7 +190,8 @@ etree_status etree_verify_attn_paged(const etree_batch *batch, const int32_t *bl
  *   lse      [n_total][hq][2] fp32 log-sum-exp of each map's scaled scores; may be NULL
  * scale must be positive.  Other arguments, limits and errors as etree_verify_attn, with a
  * workspace of etree_attn_diff_workspace_size bytes (0 for invalid arguments).  Maxima, sums and
- * both maps' outputs are held in fp32; probabilities are rounded to bf16 for their product with v.
+ * both maps' outputs are held in fp32; probabilities enter their product with v as two bf16 parts, off
+ * by less than 2^-14 of each.
  * Infinities and NaN in keys or values that a node does not see do not reach its output.  Output
  * rows of a request that is reported as invalid are left as they were.
  */
@@ -226,7 +227,7 @@ etree_status etree_verify_attn_diff_paged(
  * x, wq, scales and zeros are 16-byte aligned; K is a multiple of 32 up to 2^18, 0 <= M <= 65536.
  * No weight is rounded: products with the integers q - zeros are exact and added in fp32, group by
  * group, times the scale.  Results do not depend on timing.  out may not overlap an input.
- * Two launches; the workspace has etree_w4_workspace_size bytes (0 for invalid arguments).
+ * One to three launches; the workspace has etree_w4_workspace_size bytes (0 for invalid arguments).
  */
 size_t etree_w4_workspace_size(int M, int N, int K);
 etree_status etree_w4_linear(const uint16_t* x, int64_t x_stride, int M, const uint8_t* wq,
