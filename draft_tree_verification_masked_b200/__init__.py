@@ -507,6 +507,8 @@ def _work(workspace, dev: int):
 
 def _rows(t, name: str, dev: int):
     """Pointer and row stride of a [rows, heads, dims] bf16 tensor whose rows are dense inside."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
     _, h, d = t.shape
     s0, s1, s2 = t.stride()
     if t.dtype is not torch.bfloat16:
@@ -625,6 +627,8 @@ def etree_w4_linear(x, wq, scales, zeros, group: int, bias, out, workspace, stre
 
 def _matrix(t, dtype, name: str, dev: int):
     """Pointer and row stride of a [rows, columns] tensor whose rows are dense inside."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.get_device() != dev:
