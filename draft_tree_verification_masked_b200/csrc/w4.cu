@@ -218,13 +218,15 @@ template <int NT, int KS, int GPB>
 __device__ __noinline__ void w4_scales(const W4Params& p, uint8_t* smem, W4Smem* sh) {
   using Sh = W4Shape<NT, KS, GPB>;
   const int lane = threadIdx.x & 31, ng = p.K / p.group;
-  const bool wide = ng % (2 * GPB) == 0;
-  W4Row<2 * GPB, uint16_t> sc[8];
-  W4Row<2 * GPB, uint8_t> zp[8];
+  // with two row tiles a unit's groups lie behind the last one's: loaded for two units at once
+  constexpr int kU = KS == 2 && GPB <= 2 ? 2 : 1;
+  const bool wide = ng % (2 * GPB * kU) == 0;
+  W4Row<2 * GPB * kU, uint16_t> sc[8];
+  W4Row<2 * GPB * kU, uint8_t> zp[8];
 #pragma unroll
   for (int r = 0; r < 8; ++r)
 #pragma unroll
-    for (int j = 0; j < Sh::kZWords; ++j) zp[r].w[j] = 0x08080808u;
+    for (int j = 0; j < zp[r].kWords; ++j) zp[r].w[j] = 0x08080808u;
   const uint16_t* srow[8];
   const uint8_t* zrow[8];
   auto rows_of = [&](int rowt) {                        // once a segment
@@ -239,7 +241,7 @@ __device__ __noinline__ void w4_scales(const W4Params& p, uint8_t* smem, W4Smem*
   auto fetch = [&](int kb) {
 #pragma unroll
     for (int half = 0; half < 2; ++half) {              // rows of warpgroup 0, then of 1
-      const int g = (kb * KS + (KS == 4 ? 2 * half : 0)) * GPB;
+      const int g = ((kb & ~(kU - 1)) * KS + (KS == 4 ? 2 * half : 0)) * GPB;
 #pragma unroll
       for (int r = 4 * half; r < 4 * half + 4; ++r) sc[r].fetch(srow[r], g, ng, wide);
       if (p.zeros) {
@@ -260,25 +262,31 @@ __device__ __noinline__ void w4_scales(const W4Params& p, uint8_t* smem, W4Smem*
   }
   while (more) {
     if (!mbar_wait(&sh->empty[st], ph)) { ok = false; break; }
+    const bool second = kU == 2 && (kb & 1);            // of the two units loaded
     uint32_t* dst = reinterpret_cast<uint32_t*>(smem + st * Sh::kStage + Sh::kTx) + lane;
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
 #pragma unroll
-      for (int j = 0; j < Sh::kSWords; ++j) dst[j * 256 + r * 32] = sc[r].w[j];
+      for (int j = 0; j < Sh::kSWords; ++j)
+        dst[j * 256 + r * 32] = second ? sc[r].w[(kU - 1) * Sh::kSWords + j] : sc[r].w[j];
 #pragma unroll
-      for (int j = 0; j < Sh::kZWords; ++j) dst[(Sh::kSWords + j) * 256 + r * 32] = zp[r].w[j];
+      for (int j = 0; j < Sh::kZWords; ++j)
+        dst[(Sh::kSWords + j) * 256 + r * 32] =
+            GPB == 1 ? zp[r].w[0] >> (second ? 16 : 0) : second ? zp[r].w[kU - 1] : zp[r].w[j];
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh->full[st]);
     if (++st == Sh::kStages) { st = 0; ph ^= 1; }
     ++kb;
+    bool load = (kb & (kU - 1)) == 0;
     if (--left == 0) {                                  // the next unit is another segment's
       more = w4_segment(p, ++seg, at);
       kb = at.kb;
       left = at.n;
       if (more) rows_of(at.rowt);
+      load = true;
     }
-    if (more) fetch(kb);
+    if (more && load) fetch(kb);
   }
   if (!ok && lane == 0) report(p.ws, ETREE_ETIMEOUT, DET_WAIT_W4);
 }
