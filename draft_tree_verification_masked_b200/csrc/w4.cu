@@ -25,8 +25,8 @@
 // the loads, two the MMAs, one brings scales and zero points, eight unpack and eight add.
 //
 // Floor of 64 tokens x 151,936 x 5,120 with fp32 output: 447 MB, 69 us at the copy rate.  Measured
-// 222 us, 2.0 TB/s; no pipe is above 35%, so it is the hand-overs between the roles that bound it,
-// and of them the scales' loads cost about 50 us.  16 tokens of the same 138 us (floor 64).
+// 196 us, 2.3 TB/s; no pipe is above 40%, so it is the hand-overs between the roles that bound it
+// (167 us without the scales' loads).  16 tokens of the same 119-130 us (floor 64).
 #include <algorithm>
 
 #include "kernels.cuh"
@@ -212,43 +212,51 @@ __global__ void __launch_bounds__(256) w4_prepare_kernel(W4Params p, int rows) {
   reinterpret_cast<uint4*>(p.xp)[i] = v;
 }
 
-// One warp brings the scales and zero points, a few bytes of each row: eight rows a lane, the next
-// unit's loads in flight while this one's stage is awaited.
+// One warp brings the scales and zero points, a few bytes of each row: eight rows a lane.  With two
+// row tiles a unit's groups lie behind the last one's, and eight groups are loaded at once, for 4 / GPB
+// units.  The next units' loads are in flight while a stage is awaited.
 template <int NT, int KS, int GPB>
 __device__ __noinline__ void w4_scales(const W4Params& p, uint8_t* smem, W4Smem* sh) {
   using Sh = W4Shape<NT, KS, GPB>;
+  constexpr int kU = KS == 2 ? 4 / GPB : 1, kGroups = 2 * GPB * kU;
   const int lane = threadIdx.x & 31, ng = p.K / p.group;
-  // with two row tiles a unit's groups lie behind the last one's: loaded for two units at once
-  constexpr int kU = KS == 2 && GPB <= 2 ? 2 : 1;
-  const bool wide = ng % (2 * GPB * kU) == 0;
-  W4Row<2 * GPB * kU, uint16_t> sc[8];
-  W4Row<2 * GPB * kU, uint8_t> zp[8];
+  const bool wide = ng % kGroups == 0;
+  W4Row<kGroups, uint16_t> sc[8];
+  W4Row<kGroups, uint8_t> zp[8];
 #pragma unroll
   for (int r = 0; r < 8; ++r)
 #pragma unroll
     for (int j = 0; j < zp[r].kWords; ++j) zp[r].w[j] = 0x08080808u;
-  const uint16_t* srow[8];
-  const uint8_t* zrow[8];
+  int64_t base = 0;                                     // the tile's first row, in elements
+  int off[8];                                           // this lane's rows behind it
   auto rows_of = [&](int rowt) {                        // once a segment
+    base = (int64_t)rowt * Sh::kRows * ng;
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
       const int i = r * 32 + lane;                      // row i of the unit's 2 x 128
-      const int n = min(rowt * Sh::kRows + (KS == 4 ? i & 127 : i), p.N - 1);
-      srow[r] = p.scales + (int64_t)n * ng;
-      zrow[r] = p.zeros + (int64_t)n * ng;
+      off[r] = min(KS == 4 ? i & 127 : i, p.N - 1 - rowt * Sh::kRows) * ng;
     }
   };
   auto fetch = [&](int kb) {
+    const uint16_t* s = p.scales + base;
+    const uint8_t* z = p.zeros + base;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {              // rows of warpgroup 0, then of 1
       const int g = ((kb & ~(kU - 1)) * KS + (KS == 4 ? 2 * half : 0)) * GPB;
 #pragma unroll
-      for (int r = 4 * half; r < 4 * half + 4; ++r) sc[r].fetch(srow[r], g, ng, wide);
+      for (int r = 4 * half; r < 4 * half + 4; ++r) sc[r].fetch(s + off[r], g, ng, wide);
       if (p.zeros) {
 #pragma unroll
-        for (int r = 4 * half; r < 4 * half + 4; ++r) zp[r].fetch(zrow[r], g, ng, wide);
+        for (int r = 4 * half; r < 4 * half + 4; ++r) zp[r].fetch(z + off[r], g, ng, wide);
       }
     }
+  };
+  // word i of an array in registers
+  auto pick = [](const uint32_t* w, int n, int i) {
+    uint32_t v = w[0];
+#pragma unroll
+    for (int j = 1; j < n; ++j) v = i == j ? w[j] : v;
+    return v;
   };
   W4Segment at;
   int seg = 0;
@@ -261,18 +269,20 @@ __device__ __noinline__ void w4_scales(const W4Params& p, uint8_t* smem, W4Smem*
     fetch(kb);
   }
   while (more) {
+    const int sub = kb & (kU - 1);                      // of the units loaded
     if (!mbar_wait(&sh->empty[st], ph)) { ok = false; break; }
-    const bool second = kU == 2 && (kb & 1);            // of the two units loaded
     uint32_t* dst = reinterpret_cast<uint32_t*>(smem + st * Sh::kStage + Sh::kTx) + lane;
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
 #pragma unroll
       for (int j = 0; j < Sh::kSWords; ++j)
-        dst[j * 256 + r * 32] = second ? sc[r].w[(kU - 1) * Sh::kSWords + j] : sc[r].w[j];
+        dst[j * 256 + r * 32] = kU == 1 ? sc[r].w[j] : pick(sc[r].w, sc[r].kWords, sub * GPB + j);
 #pragma unroll
       for (int j = 0; j < Sh::kZWords; ++j)
         dst[(Sh::kSWords + j) * 256 + r * 32] =
-            GPB == 1 ? zp[r].w[0] >> (second ? 16 : 0) : second ? zp[r].w[kU - 1] : zp[r].w[j];
+            kU == 1    ? zp[r].w[j]
+            : GPB == 1 ? pick(zp[r].w, zp[r].kWords, sub >> 1) >> (16 * (sub & 1))
+                       : pick(zp[r].w, zp[r].kWords, sub);
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh->full[st]);
