@@ -58,6 +58,7 @@ constexpr int kDThreads = 32 * 12;
 struct DiffSmem {
   uint64_t kv_full[kDStages], kv_empty[kDStages], q_full, drain[2];
   uint64_t s_full[2][2], p_full[2][2], o_done[2];
+  uint64_t v_clean[2];                      // V of the cache's last tile, and of the tree's
   uint64_t anc[64];
   unsigned long long bad;                   // tree nodes whose V holds an infinity or NaN
   int32_t par[64];
@@ -187,6 +188,7 @@ attn_diff_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     }
     mbar_init(&sh->q_full, 1);
     for (int m = 0; m < 2; ++m) {
+      mbar_init(&sh->v_clean[m], 8);
       mbar_init(&sh->o_done[m], 1);
       mbar_init(&sh->drain[m], 1);
       for (int b = 0; b < 2; ++b) {
@@ -346,11 +348,12 @@ attn_diff_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     for (int j = 0; ok && j < T; ++j) {
       const int b = j & 1, t = t0 + j;
       const uint32_t ph = (j >> 1) & 1;
-      // each map's warps clean one half of V in a tile with masked keys (at most the last two):
-      // both must be done
+      // each map's warps clean one half of V in a tile with masked keys: both must be done.  These
+      // tiles (at most the cache's last and the tree's) have a barrier each that completes once, since
+      // the maps may run apart by more than the two tiles that p_full's phases tell from each other.
       const bool masked = t >= nt_cache || L - t * kDKeys < kDKeys;
       if (!mbar_wait(&sh->p_full[m][b], ph)) { ok = false; break; }
-      if (masked && !mbar_wait(&sh->p_full[1 - m][b], ph)) { ok = false; break; }
+      if (masked && !mbar_wait(&sh->v_clean[t >= nt_cache], 0)) { ok = false; break; }
       tc_fence_after();
       const uint64_t dv = dv0 + (uint64_t)(vs * (kDKV >> 4));
       const uint32_t pa = tmem + kDS + 128 * m + 64 * b;
@@ -430,6 +433,8 @@ attn_diff_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         }
         if (bad) atomicOr(&sh->bad, bad);
         fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->v_clean[t >= nt_cache]);
       }
       if (work) {
         if (masked) {
