@@ -58,6 +58,7 @@ constexpr int kDThreads = 32 * 12;
 struct DiffSmem {
   uint64_t kv_full[kDStages], kv_empty[kDStages], q_full, drain[2];
   uint64_t s_full[2][2], p_full[2][2], o_done[2];
+  uint64_t o_final[2];                      // the last product of a map is done
   uint64_t v_clean[2];                      // V of the cache's last tile, and of the tree's
   uint64_t anc[64];
   unsigned long long bad;                   // tree nodes whose V holds an infinity or NaN
@@ -190,6 +191,7 @@ attn_diff_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     for (int m = 0; m < 2; ++m) {
       mbar_init(&sh->v_clean[m], 8);
       mbar_init(&sh->o_done[m], 1);
+      mbar_init(&sh->o_final[m], 1);
       mbar_init(&sh->drain[m], 1);
       for (int b = 0; b < 2; ++b) {
         mbar_init(&sh->s_full[m][b], 1);
@@ -366,6 +368,7 @@ attn_diff_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         for (int k = 0; k < kDKeys / 16; ++k)           // what the first part left
           tc_mma_bf16_ts(tmem + 128 * m, pa + 32 + 8 * k, dv + k * (2048 >> 4), idO, 1u);
         tc_commit(&sh->o_done[m]);
+        if (j + 1 == T) tc_commit(&sh->o_final[m]);
         tc_commit(&sh->kv_empty[vs]);
       }
       __syncwarp();
@@ -481,7 +484,8 @@ attn_diff_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const float corr = need ? ex2_approx(m_ref - m_new) : 1.f;
         l = l * corr + (a0 + a1);
         m_ref = m_new;
-        // A rescale of O_m needs every earlier product of this map finished (the last wrote O_m).
+        // A rescale of O_m needs every earlier product of this map finished.  The one of tile j - 2
+        // is: S of tile j was issued behind it.
         if (any && j >= 1) {
           if (!mbar_wait(&sh->o_done[m], (j - 1) & 1)) { ok = false; break; }
           tc_fence_after();
@@ -501,7 +505,8 @@ attn_diff_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->p_full[m][j & 1]);
     }
-    if (ok && !mbar_wait(&sh->o_done[m], (T - 1) & 1)) ok = false;
+    // not o_done: its product of tile T - 2 may still run, and that phase would pass for T - 1's
+    if (ok && !mbar_wait(&sh->o_final[m], 0)) ok = false;
     if (!ok) report(p.ws, ETREE_ETIMEOUT, DET_WAIT_ATTN);
     tc_fence_after();
     const int h = kvh * G + g;

@@ -344,7 +344,8 @@ def test_equal_maps_cancel():
 @pytest.mark.parametrize("page", [0, 16])
 def test_many_calls_give_the_same_bits(page):
     """Caches that end inside a tile, with unused rows that are not finite: the two maps of a CTA clean
-    the last tiles' values together, whichever runs ahead."""
+    the last tiles' values together, whichever runs ahead, and the outputs wait for the last products
+    of both, however short the last tile's softmax."""
     c = Case([6, 4, 1, 17] * 9, [37, 101, 230, 333] * 9, 8, 2, page=page, norm=False, seed=41)
     used = np.zeros(c.kc_h.shape[0], bool)
     for rows in c.rows:
