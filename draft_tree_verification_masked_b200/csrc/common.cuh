@@ -40,7 +40,7 @@ enum Detail : int32_t {
   DET_WAIT_WALK = 13,       // the tree walk gave up waiting for another CTA's residual slice
   DET_FREE_RING = 14,       // the free ring's head and tail do not fit its pages (etree_page_plan)
   DET_BAD_SLOT = 15,        // a slot below -1 or past the pool (etree_kv_store)
-  DET_WAIT_W4 = 16,         // a bounded wait gave up in a 4-bit product
+  DET_WAIT_PRODUCT = 16,    // a bounded wait gave up in a 4-bit product
 };
 
 __device__ __forceinline__ void report(WsHeader* ws, int32_t code, int32_t detail) {

@@ -298,7 +298,7 @@ __device__ __noinline__ void w4_scales(const W4Params& p, uint8_t* smem, W4Smem*
     }
     if (more && load) fetch(kb);
   }
-  if (!ok && lane == 0) report(p.ws, ETREE_ETIMEOUT, DET_WAIT_W4);
+  if (!ok && lane == 0) report(p.ws, ETREE_ETIMEOUT, DET_WAIT_PRODUCT);
 }
 
 // The two roles with many live registers are functions of their own, so that each is allocated
@@ -368,7 +368,7 @@ __device__ __noinline__ void w4_unpack(const W4Params& p, uint8_t* smem, W4Smem*
       src = src0;
     }
   }
-  if (!ok && lane == 0) report(p.ws, ETREE_ETIMEOUT, DET_WAIT_W4);
+  if (!ok && lane == 0) report(p.ws, ETREE_ETIMEOUT, DET_WAIT_PRODUCT);
 }
 
 // Summing: warpgroup wg adds the scaled group sums of blocks 2 wg and 2 wg + 1, and writes the tile.
@@ -491,7 +491,7 @@ __device__ __noinline__ void w4_sum(const W4Params& p, const uint8_t* smem, floa
     }
     if constexpr (KS == 4) w4_sync();                   // `red` is free again
   }
-  if (!ok && lane == 0) report(p.ws, ETREE_ETIMEOUT, DET_WAIT_W4);
+  if (!ok && lane == 0) report(p.ws, ETREE_ETIMEOUT, DET_WAIT_PRODUCT);
 }
 
 template <int NT, int KS, int GPB>
@@ -575,7 +575,7 @@ w4_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
       // are none: the loop above reaches every unit that was loaded ahead
       for (int i = max(0, issued - kStages); i < issued; ++i)
         ok = mbar_wait(&sh->full[i % kStages], (i / kStages) & 1) && ok;
-      if (!ok) report(p.ws, ETREE_ETIMEOUT, DET_WAIT_W4);
+      if (!ok) report(p.ws, ETREE_ETIMEOUT, DET_WAIT_PRODUCT);
     }
   } else if (warp == 1 || warp == 2) {
     // ------------------------------------------------- MMA issuers, two of the four blocks each
@@ -624,7 +624,7 @@ w4_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
     if (elect_one()) tc_commit(&sh->drain[warp - 1]);
     __syncwarp();
     if (!mbar_wait(&sh->drain[warp - 1], 0)) ok = false;
-    if (!ok && lane == 0) report(p.ws, ETREE_ETIMEOUT, DET_WAIT_W4);
+    if (!ok && lane == 0) report(p.ws, ETREE_ETIMEOUT, DET_WAIT_PRODUCT);
   } else if (warp == 3) {
     w4_scales<NT, KS, GPB>(p, smem, sh);
   } else if (warp < 12) {

@@ -523,6 +523,7 @@ etree_status etree_plan_tree(const etree_cost_table *table, int32_t B, int32_t L
  *   13  walk wait: the tree walk gave up waiting for another CTA's part of a residual sum
  *   14  free ring: a free ring whose head and tail do not fit its pages (etree_page_plan)
  *   15  bad slot: a slot below -1 or past the pool (etree_kv_store)
+ *   16  product wait: a bounded wait gave up in a 4-bit product (etree_w4_linear)
  */
 etree_status etree_device_status(void *workspace, void *stream, int32_t *detail);
 

@@ -1,6 +1,8 @@
 """Host-side refusals of the serving operators: every call below fails a host check before any
 device work, so fake addresses are never dereferenced."""
 import ctypes as C
+import os
+import re
 
 import pytest
 
@@ -170,3 +172,16 @@ def test_w4_refusals(L):
     _rejects(lin(wsb=need - 1), -1, "workspace")
     assert L.etree_w4_workspace_size(4, 0, 256) == 0 and L.etree_w4_workspace_size(4, 100, 250) == 0
     assert lin(M=0, x=None, out=None) == 0                   # no tokens: no device work
+
+
+def test_every_detail_code_of_the_kernels_is_documented_and_named(L):
+    """Digits in a code's name included: the header's list, the kernels' enum and the binding."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    with open(os.path.join(root, "draft_tree_verification_masked_b200", "csrc", "common.cuh")) as f:
+        enum = {int(v) for _, v in re.findall(r"\b(DET_[A-Z0-9_]+)\s*=\s*(\d+)", f.read())}
+    with open(os.path.join(root, "include", "etree.h")) as f:
+        hdr = f.read()
+    block = hdr[hdr.index("Detail codes:"):hdr.index("etree_device_status(void")]
+    listed = {int(n) for n in re.findall(r"\n \*\s+(\d+)\s+[a-z0-9]", block)}
+    assert len(enum) == max(enum) + 1
+    assert enum == listed == set(et.DETAIL)
