@@ -296,21 +296,40 @@ typedef CUresult (*CtxGetIdFn)(CUcontext, unsigned long long*);
 static std::mutex g_scratch_mu;
 static std::unordered_map<unsigned long long, void*> g_scratch_ptr;
 
-// Device address of g_attn_scratch in the calling thread's current context.
-static etree_status static_scratch(void** out) {
-  static CtxGetCurrentFn get_current = nullptr;
-  static CtxGetIdFn get_id = nullptr;
+// The driver's calls for the current context and its id, null where the driver lacks them.
+struct ContextFns {
+  CtxGetCurrentFn get_current = nullptr;
+  CtxGetIdFn get_id = nullptr;
+};
+
+static const ContextFns& context_fns() {
+  static ContextFns fns;
   static std::once_flag once;
   std::call_once(once, [] {
     void* p = nullptr;
     cudaDriverEntryPointQueryResult q;
     if (cudaGetDriverEntryPoint("cuCtxGetCurrent", &p, cudaEnableDefault, &q) == cudaSuccess &&
         q == cudaDriverEntryPointSuccess)
-      get_current = reinterpret_cast<CtxGetCurrentFn>(p);
+      fns.get_current = reinterpret_cast<CtxGetCurrentFn>(p);
     if (cudaGetDriverEntryPoint("cuCtxGetId", &p, cudaEnableDefault, &q) == cudaSuccess &&
         q == cudaDriverEntryPointSuccess)
-      get_id = reinterpret_cast<CtxGetIdFn>(p);
+      fns.get_id = reinterpret_cast<CtxGetIdFn>(p);
   });
+  return fns;
+}
+
+unsigned long long current_context_id() {
+  const ContextFns& fns = context_fns();
+  CUcontext ctx = nullptr;
+  unsigned long long id = 0;
+  if (!fns.get_current || !fns.get_id || fns.get_current(&ctx) != CUDA_SUCCESS || !ctx) return 0;
+  return fns.get_id(ctx, &id) == CUDA_SUCCESS ? id : 0;
+}
+
+// Device address of g_attn_scratch in the calling thread's current context.
+static etree_status static_scratch(void** out) {
+  const CtxGetCurrentFn get_current = context_fns().get_current;
+  const CtxGetIdFn get_id = context_fns().get_id;
   if (!get_current || !get_id)
     return fail(ETREE_ECUDA, "etree_verify_attn_noalloc: cuCtxGetCurrent / cuCtxGetId unavailable");
   CUcontext ctx = nullptr;

@@ -377,25 +377,26 @@ __device__ __forceinline__ void pdl_trigger() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// The id of the calling thread's current context, unique for the life of the process, or 0 if the thread
+// has none yet or the driver cannot tell (api.cu).
+unsigned long long current_context_id();
+
 // Raises a kernel's dynamic shared memory limit to `bytes`, the one size it is launched with: once
-// per device (the attribute belongs to the device's context and stays).
+// per context, to which the attribute belongs (a device reset or a context of the caller's starts anew).
 template <typename... KArgs>
 static cudaError_t raise_smem_once(void (*kernel)(KArgs...), int bytes) {
+  constexpr unsigned kRemembered = 64;
   static std::mutex mu;
-  static struct { const void* kernel; int dev; } done[64];
-  static int count = 0;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
+  static struct { const void* kernel; unsigned long long ctx; } done[kRemembered];
+  static unsigned count = 0;
   const void* k = reinterpret_cast<const void*>(kernel);
+  const unsigned long long ctx = current_context_id();
   std::lock_guard<std::mutex> lk(mu);
-  for (int i = 0; i < count; ++i)
-    if (done[i].kernel == k && done[i].dev == dev) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess && count < 64) {                 // past that, it is set at every call
-    done[count].kernel = k;
-    done[count++].dev = dev;
-  }
+  if (ctx)
+    for (const auto& d : done)
+      if (d.kernel == k && d.ctx == ctx) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && ctx) done[count++ % kRemembered] = {k, ctx};   // the oldest is forgotten
   return e;
 }
 
