@@ -361,3 +361,31 @@ def test_many_calls_give_the_same_bits(page):
         c.call()
         assert torch.equal(c.out, first)
     c.check(range(4))
+
+
+@pytest.mark.parametrize("page", [0, 16, 128])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -3.3e38])
+@pytest.mark.parametrize("kv", [[70, 31], [64, 128], [2900, 1]])
+def test_values_in_masked_places_change_no_bit(page, value, kv):
+    """`value` in keys and values of a leaf, of the cache rows behind kv_len and of every unused row: the rows
+    that do not see it keep their bits, and every row of a clean leaf is within the derived tolerance."""
+    c = Case([6, 3], kv, 4, 2, page=page, seed=7)
+    c.parent[:6] = [-1, 0, 1, 0, 0, 0]       # a chain 0-1-2, and leaves 3, 4, 5 under the root
+    c.dev["parent"].copy_(torch.from_numpy(c.parent))
+    c.run()
+    out, lse = c.out.clone(), c.lse.clone()
+    used = np.zeros(c.kc_h.shape[0], bool)
+    for rows in c.rows:
+        used[rows] = True
+    for d in (c.kc, c.vc):
+        d[torch.from_numpy(~used).cuda()] = value
+    c.call()
+    torch.cuda.synchronize()
+    assert torch.equal(c.out, out) and torch.equal(c.lse, lse)
+    for d in (c.kt, c.vt):
+        d[4] = value
+    c.call()
+    assert et.etree_device_status(c.ws) == (0, 0)
+    keep = [i for i in range(c.nt) if i != 4]
+    assert torch.equal(c.out[keep], out[keep]) and torch.equal(c.lse[keep], lse[keep])
+    assert not torch.equal(c.out[4], out[4])                 # node 4 does see itself
