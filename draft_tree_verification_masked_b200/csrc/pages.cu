@@ -30,7 +30,7 @@ constexpr int kPlanThreads = 256;
 struct PlanScan {
   long long warp_g[kPlanThreads / 32], warp_r[kPlanThreads / 32], warp_a[kPlanThreads / 32];
   long long taken, back, head, tail;
-  int ring_ok;
+  int decreasing;                             // cu_new is: a search by halves does not find every token
 };
 
 __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanParams p) {
@@ -55,6 +55,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanParams p) {
   if (tid == 0) {
     sc.head = p.ring_state[0];
     sc.tail = p.ring_state[1];
+    sc.decreasing = 0;
   }
   __syncthreads();
   const long long head = sc.head, tail = sc.tail;
@@ -71,6 +72,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanParams p) {
     const long long len = (long long)kv_s[r] + n;
     const int held = held_s[r];
     int code = 0;
+    if (n < 0) sc.decreasing = 1;
     if (n < 0 || cu_s[r] < 0 || (p.slot_map && cu_s[r + 1] > p.n_tokens) || (r == 0 && cu_s[0] != 0))
       code = DET_BAD_NODES;
     else if (kv_s[r] < 0 || held < 0 || held > p.max_pages ||
@@ -184,7 +186,15 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanParams p) {
   for (long long i = i0; i < p.n_tokens; i += stride) {
     const int j = (int)i;
     long long slot = -1;
-    const int r = find(cu_s + 1, j);
+    int r;
+    if (!sc.decreasing) {
+      r = find(cu_s + 1, j);
+    } else {                                  // the first valid range that holds the token
+      for (r = 0; r < B - 1; ++r)
+        if (j >= cu_s[r] && j < cu_s[r + 1] && cu_s[r] >= 0 && cu_s[r + 1] <= p.n_tokens &&
+            (r > 0 || cu_s[0] == 0))
+          break;
+    }
     const int kv = kv_s[r];
     if (kv >= 0 && j >= cu_s[r] && j < cu_s[r + 1]) {
       const int t = kv + (j - cu_s[r]);

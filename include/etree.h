@@ -403,7 +403,8 @@ etree_status etree_kv_compact_paged(const etree_batch *batch, const int32_t *blo
  * may overlap an input or another output (ETREE_EINVAL).  The workspace needs only its 256-byte
  * status header.  A request with new_r < 0 or cu_new out of range (ETREE_EDEVICE, detail 2), with
  * a negative length, pages_held outside [0, max_pages] or more tokens than max_pages hold
- * (detail 3) is left as it is, its slots -1.  A ring state that does not fit the ring, before or
+ * (detail 3) is left as it is, its slots -1; where a decreasing cu_new lets ranges overlap, a token is
+ * the first request's whose range is in order.  A ring state that does not fit the ring, before or
  * with the pages given back, records detail 14: nothing is then given back (nor taken, when the
  * state itself is wrong).  A page id outside [0, num_pages) under a new token records detail 11 and
  * its slot is -1.  Two calls that share a ring or a block table must be ordered.

@@ -287,3 +287,29 @@ def test_store_past_32_bit_offsets():
     for p in (pool, vpool):
         assert torch.equal(p[at].view(torch.int16), k.view(torch.int16))
         assert int((p.view(torch.int16) != 0).any(-1).any(-1).sum()) == 2
+
+
+@pytest.mark.parametrize("cu", [[0, 8, 2, 4, 6], [0, 5, 3, 15, 20], [0, 4, 2, 2, 9], [0, 2, 90, 5, 12],
+                                [0, 3, 6, 1, 4]])
+def test_a_decreasing_start_costs_other_requests_no_slot(cu):
+    """Requests with a bad range keep what they hold; every token inside a valid range gets a slot, the first
+    such request's where ranges overlap."""
+    B, n_tokens = 4, 20
+    held = [1, 2, 0, 3]
+    pool = Pool(B, 16, 4, 24, held)
+    kv = np.array([3, 20, 0, 40], np.int32)
+    slot = torch.full((n_tokens,), SENT, dtype=torch.int64, device="cuda")
+    et.etree_page_plan(torch.tensor(cu, dtype=torch.int32, device="cuda"), torch.from_numpy(kv).cuda(), 16, 24,
+                       pool.d_held[0], pool.d_ring, pool.d_state[0], pool.d_bt, pool.d_held[1],
+                       pool.d_state[1], None, slot, pool.ws)
+    assert et.etree_device_status(pool.ws) == (EDEVICE, 2)
+    bt, got = pool.d_bt.cpu().numpy(), slot.cpu().numpy()
+    want = np.full(n_tokens, -1, np.int64)
+    for r in reversed(range(B)):
+        if 0 <= cu[r] <= cu[r + 1] <= n_tokens:
+            t = kv[r] + np.arange(cu[r + 1] - cu[r])
+            want[cu[r]:cu[r + 1]] = bt[r, t // 16].astype(np.int64) * 16 + t % 16
+            assert int(pool.d_held[1][r]) == -(-(kv[r] + cu[r + 1] - cu[r]) // 16)
+        else:
+            assert int(pool.d_held[1][r]) == held[r]
+    assert np.array_equal(got, want)
