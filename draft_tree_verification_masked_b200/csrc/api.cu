@@ -709,6 +709,9 @@ struct DiffPlan {
   int G, nb, mchunks, nsplit, tps;
 };
 constexpr int kDiffStart = 6, kDiffMerge = 8;
+constexpr int kDiffWaves = 4;               // split launches have at most this many CTAs an SM
+
+static int diff_tiles(const etree_batch* b) { return (int)(((int64_t)b->kv_len_max + 63) / 64) + 1; }
 
 static DiffPlan plan_diff(const etree_batch* b, int hq, int hkv) {
   DiffPlan pl{};
@@ -717,11 +720,11 @@ static DiffPlan plan_diff(const etree_batch* b, int hq, int hkv) {
   pl.mchunks = (b->n_max + pl.nb - 1) / pl.nb;
   const int64_t pairs = (int64_t)b->B * hkv * pl.mchunks;
   const int sms = sm_count();
-  const int tiles = (int)(((int64_t)b->kv_len_max + 63) / 64) + 1;
+  const int tiles = diff_tiles(b);
   int64_t best = INT64_MAX;
   pl.tps = tiles;
   for (int ns = 1; ns <= std::min(tiles, 2 * sms); ++ns) {
-    if (ns > 1 && pairs * ns > 4 * (int64_t)sms) break;
+    if (ns > 1 && pairs * ns > kDiffWaves * (int64_t)sms) break;
     const int tps = (tiles + ns - 1) / ns;
     const int64_t c = (pairs * ns + sms - 1) / sms;
     const int64_t cost = c * (tps + kDiffStart) + (ns > 1 ? kDiffMerge : 0);
@@ -738,9 +741,15 @@ struct DiffLayout {
   size_t order, o_part, ml_part, total;
 };
 
+// Room for the partial rows of this batch and of every batch of these heads with no more requests,
+// nodes, nodes a request and cached tokens, which may split its keys where this one does not.  A split
+// launch has at most kDiffWaves CTAs an SM with G * nb rows each, and no more parts of a row than tiles.
 static DiffLayout diff_layout(const etree_batch* b, const DiffPlan& pl, int hq) {
   DiffLayout w{};
-  const size_t parts = pl.nsplit > 1 ? (size_t)b->n_total * hq * pl.nsplit * 2 : 0;
+  const int64_t tiles = diff_tiles(b);
+  const int64_t rows = std::min((int64_t)b->n_total * hq * tiles,
+                                (int64_t)kDiffWaves * sm_count() * pl.G * pl.nb);
+  const size_t parts = tiles > 1 ? (size_t)rows * 2 : 0;
   w.order = up256(sizeof(WsHeader));
   w.o_part = up256(w.order + (size_t)b->B * sizeof(int32_t));
   w.ml_part = up256(w.o_part + parts * 128 * sizeof(float));

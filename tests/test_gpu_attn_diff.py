@@ -389,3 +389,14 @@ def test_values_in_masked_places_change_no_bit(page, value, kv):
     keep = [i for i in range(c.nt) if i != 4]
     assert torch.equal(c.out[keep], out[keep]) and torch.equal(c.lse[keep], lse[keep])
     assert not torch.equal(c.out[4], out[4])                 # node 4 does see itself
+
+
+def test_one_workspace_as_requests_finish():
+    """A workspace made for the first batch serves the smaller ones after it, whose keys are split."""
+    nodes, kv = [6, 3, 1, 6] * 20, [5000, 300, 4097, 2600] * 20
+    ws = None
+    for B in (80, 33, 5, 1):
+        c = Case(nodes[:B], kv[:B], 8, 2, page=16, seed=B)
+        ws = c.ws if ws is None else ws
+        c.ws = ws
+        c.run(range(min(B, 3)))

@@ -2,6 +2,7 @@
 device work, so fake addresses are never dereferenced."""
 import ctypes as C
 import os
+import random
 import re
 
 import pytest
@@ -185,3 +186,34 @@ def test_every_detail_code_of_the_kernels_is_documented_and_named(L):
     listed = {int(n) for n in re.findall(r"\n \*\s+(\d+)\s+[a-z0-9]", block)}
     assert len(enum) == max(enum) + 1
     assert enum == listed == set(et.DETAIL)
+
+
+@pytest.mark.parametrize("hq,hkv", [(40, 8), (8, 2), (64, 1), (3, 3)])
+def test_attn_diff_workspace_serves_every_smaller_batch(L, hq, hkv):
+    """Keys are split only where requests are few, so a smaller batch needs partial results that a larger one
+    does not: the size holds for both."""
+    def size(B, n_total, n_max, kv):
+        b = _batch(B=B, n_total=n_total, n_max=n_max, kv_len_max=kv)
+        return L.etree_attn_diff_workspace_size(C.byref(b), hq, hkv)
+
+    rs = random.Random(hq)
+    for _ in range(300):
+        B, n_max, kv = rs.choice([1, 4, 16, 64, 300, 4096]), rs.randint(1, 64), rs.choice([0, 70, 8192, 131072])
+        n_total = rs.randint(max(B, B * n_max // 2), B * n_max)
+        if n_total * hq > 1 << 26:
+            continue
+        whole = size(B, n_total, n_max, kv)
+        assert 0 < whole < 1 << 30
+        for _ in range(20):
+            b, n, k = rs.randint(1, B), rs.randint(1, n_max), rs.randint(0, kv)
+            if b <= n_total:
+                nt = rs.randint(b, min(n_total, b * n))
+                assert size(b, nt, n, k) <= whole, (B, n_total, n_max, kv, b, nt, n, k)
+
+
+def test_w4_workspace_serves_every_smaller_product(L):
+    rs = random.Random(0)
+    for _ in range(2000):
+        M, N, K = rs.randint(1, 300), rs.randint(1, 60000), 32 * rs.randint(1, 300)
+        m, n, k = rs.randint(1, M), rs.randint(1, N), 32 * rs.randint(1, K // 32)
+        assert L.etree_w4_workspace_size(m, n, k) <= L.etree_w4_workspace_size(M, N, K), (M, N, K, m, n, k)
