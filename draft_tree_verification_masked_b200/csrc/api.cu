@@ -763,8 +763,16 @@ static etree_status check_heads(int hq, int hkv) {
   return ETREE_OK;
 }
 
+static etree_status check_diff_rows(const etree_batch* b, int hq, int hkv) {
+  if ((int64_t)b->n_total * hq > (int64_t)1 << 26 || (int64_t)b->B * hkv * b->n_max >= INT32_MAX)
+    return fail(ETREE_EINVAL, "n_total=%d with hq=%d: too many rows", b->n_total, hq);
+  return ETREE_OK;
+}
+
 size_t etree_attn_diff_workspace_size(const etree_batch* batch, int hq, int hkv) {
-  if (check_batch(batch) != ETREE_OK || check_heads(hq, hkv) != ETREE_OK) return 0;
+  if (check_batch(batch) != ETREE_OK || check_heads(hq, hkv) != ETREE_OK ||
+      check_diff_rows(batch, hq, hkv) != ETREE_OK)
+    return 0;
   return diff_layout(batch, plan_diff(batch, hq, hkv), hq).total;
 }
 
@@ -790,8 +798,7 @@ static etree_status attn_diff_impl(const etree_batch* b, const uint16_t* q, int6
     if (x.stride < (int64_t)x.heads * head_dim || x.stride % 8 || x.stride >= (int64_t)1 << 38)
       return fail(ETREE_EINVAL, "%s=%lld: need a multiple of 8 of at least %d heads", x.name,
                   (long long)x.stride, x.heads);
-  if ((int64_t)b->n_total * hq > (int64_t)1 << 26 || (int64_t)b->B * hkv * b->n_max >= INT32_MAX)
-    return fail(ETREE_EINVAL, "n_total=%d with hq=%d: too many rows", b->n_total, hq);
+  if ((st = check_diff_rows(b, hq, hkv))) return st;
   const DiffPlan pl = plan_diff(b, hq, hkv);
   const DiffLayout w = diff_layout(b, pl, hq);
   if (!workspace || ((uintptr_t)workspace & 255))

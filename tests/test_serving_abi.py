@@ -217,3 +217,13 @@ def test_w4_workspace_serves_every_smaller_product(L):
         M, N, K = rs.randint(1, 300), rs.randint(1, 60000), 32 * rs.randint(1, 300)
         m, n, k = rs.randint(1, M), rs.randint(1, N), 32 * rs.randint(1, K // 32)
         assert L.etree_w4_workspace_size(m, n, k) <= L.etree_w4_workspace_size(M, N, K), (M, N, K, m, n, k)
+
+
+def test_attn_diff_workspace_size_is_zero_for_batches_the_call_refuses(L):
+    """More rows than a call takes: refused alike by the call and by the size."""
+    b = _batch(B=4096, n_total=4096 * 64, n_max=64)
+    for hq, hkv in ((512, 64), (2 ** 30, 2 ** 25), (2 ** 30, 2 ** 30)):
+        assert L.etree_attn_diff_workspace_size(C.byref(b), hq, hkv) == 0
+        _rejects(L.etree_verify_attn_diff(C.byref(b), _p(20), hq * 128, _p(21), hkv * 128, _p(22), hkv * 128,
+                                          _p(23), _p(24), 1000, hq, hkv, 128, 0.125, _p(25), None, 0.0, 1.0,
+                                          _p(27), None, _p(29), 1 << 40, None), -1, "too many rows")
