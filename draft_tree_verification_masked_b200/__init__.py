@@ -198,8 +198,11 @@ def _ptr(t: torch.Tensor | None, dtype=None, name="tensor"):
 
 def _stream(stream) -> int | None:
     if stream is None:
-        # what torch.cuda.current_stream().cuda_stream gives, without its 3 us of wrapping
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        # the raw call gives the same handle without 3 us of wrapping, but torch keeps it private
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is None:
+            return torch.cuda.current_stream().cuda_stream
+        return raw(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)

@@ -6,6 +6,7 @@ import random
 import re
 
 import pytest
+import torch
 
 import draft_tree_verification_masked_b200 as et
 from draft_tree_verification_masked_b200 import _build
@@ -227,3 +228,14 @@ def test_attn_diff_workspace_size_is_zero_for_batches_the_call_refuses(L):
         _rejects(L.etree_verify_attn_diff(C.byref(b), _p(20), hq * 128, _p(21), hkv * 128, _p(22), hkv * 128,
                                           _p(23), _p(24), 1000, hq, hkv, 128, 0.125, _p(25), None, 0.0, 1.0,
                                           _p(27), None, _p(29), 1 << 40, None), -1, "too many rows")
+
+
+def test_streams_without_the_private_shortcut(monkeypatch):
+    """The current stream's handle comes from torch's public call where the raw one is not there."""
+    class Stream:
+        cuda_stream = 1234
+
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: Stream)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    assert et._stream(None) == 1234 and et._stream(77) == 77
