@@ -895,10 +895,14 @@ struct W4Plan {
   size_t xp, part, total;
 };
 
-// The one-launch kernel serves up to 8 tokens always (8 tokens of 40000 x 8192: 66 us against 84),
-// and up to 64 while (tokens, in tiles of 8) x N x K is small, where it saves the other's start
-// (64 tokens of 1000 x 2048: 6 us against 19).  Measured crossings lie between 40 M and 65 M weights
-// at 16 tokens, 20 M and 37 M at 32, and 8 M and 20 M at 64.
+// The one-launch kernel serves up to 8 tokens always, and up to 64 while (tokens, rounded up to 16, 32
+// or 64) x N x K is small, where it saves the other's start.  Measured with weights from HBM, its time
+// against the tcgen05 kernel's, K = 5120 where not named:
+//    8 tokens   40000 rows 41 us / 46, 80000 75 / 76, 151936 139 / 129 (one token 129 / 129);
+//   16 tokens   8192 rows 18.5 us / 20.9, 10240 (the last one here) 25.8 / 23.0;
+//   32 tokens   4096 rows 20.8 us / 18.9, 5120 (the last one here) 29.7 / 19.5;
+//   64 tokens   1000 rows of 2048 8.4 us / 19.3, 1600 of 5120 17.8 / 19.9, 2560 33.4 / 20.8.
+// So the bounds lie at the far end of the crossings, which were looked for with weights in L2.
 static bool w4_is_small(int M, int N, int K) {
   if (M <= 8) return true;
   if (M > 64) return false;
@@ -988,7 +992,8 @@ etree_status etree_w4_linear(const uint16_t* x, int64_t x_stride, int M, const u
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (w4_is_small(M, N, K)) {
     // two row tiles a warp read x half as often; taken where all SMs still get a CTA (8 tokens of
-    // 7168 x 5120: 8.9 us against 11.9), and two with more tokens (32 of 4800 x 5120: 20.9 against 17.8)
+    // 7168 x 5120 from HBM: 10.8 us against 14.9, of 2560 x 5120 8.1 against 7.5), and two CTAs with more
+    // tokens (32 of 4800 x 5120: 20.9 against 17.8 with weights in L2, but 22.9 against 29.1 from HBM)
     const int mt = N >= (M <= 16 ? 32 : 64) * sm_count() ? 2 : 1;
     const cudaError_t e = launch_w4_small(p, mt, s);
     return e == cudaSuccess ? ETREE_OK : cuda_fail(e, "etree_w4_linear launch");

@@ -28,12 +28,14 @@
 // the one rounding of `out`.  O is rescaled only when a row's maximum grows by more than 2^8.
 //
 // Floor of 64 ragged requests (16 nodes, 40 query heads, 8 KV heads, 1K to 8K cached): 1.23 GB of
-// cache, 190 us at the copy rate.  Measured 331 us, 3.7 TB/s (274 us with P rounded to one bf16);
-// 128K cached tokens of one request 158 us (floor 83; 125-130); one request with 64 nodes over 4K
-// 32 us (floor 5; 30).  What bounds it is the softmax of a tile, instruction by instruction: about
-// 1 us from one S to the next.  Measured on the ragged batch with one bf16 P and not kept: sixteen
-// softmax warps with 32 keys each 291 us, the two maps' exponentials taking turns 287 us, half of
-// the exponentials as polynomials on the FMA units 331 us.
+// cache, 190 us at the copy rate.  Measured 358 us after a rest, at 1,965 MHz (3.4 TB/s), and 415 us
+// in a loop, which meets the power limit at about 1,600 MHz; 128K cached tokens of one request 166
+// and 187 us (floor 83); one request with 64 nodes over 4K 33 us (floor 5).  What bounds it is the
+// softmax of a tile, instruction by instruction: about 1 us from one S to the next.  Best of eight
+// runs, P rounded to one bf16 took 274 us on the ragged batch where two parts took 331, 125 to 130
+// against 158 on the long cache and 30 against 32 on the 64 nodes.  Measured with one bf16 P in the
+// same way and not kept: sixteen softmax warps with 32 keys each 291 us, the two maps' exponentials
+// taking turns 287 us, half of the exponentials as polynomials on the FMA units 331 us.
 //
 // A key that no row may see takes no part: V rows behind the last cached key and behind the last
 // tree node are zeroed in shared memory (0 x NaN would be NaN), and a tree node's infinite or NaN

@@ -13,7 +13,8 @@
 // ever rounded.
 //
 //   q -> bf16   a thread owns one row: (w >> 4 p) & 0x000f000f | 0x43004300 is the pair
-//               (128 + q_p, 128 + q_{p+4}), and subtracting 128 + z is exact.  The pairs go to
+//               (128 + q_p, 128 + q_{p+4}), and subtracting 128 + z is exact (integers made from bit
+//               patterns: Kim et al., "Who Says Elephants Can't Run", 2022).  The pairs go to
 //               TMEM as A.  x is copied once per call with every eight values in the matching
 //               order 0 4 1 5 2 6 3 7.
 //   D = A x^T   tcgen05.mma M=128 x N=NT x K=16, A from TMEM, x from shared memory.
@@ -25,8 +26,10 @@
 // the loads, two the MMAs, one brings scales and zero points, eight unpack and eight add.
 //
 // Floor of 64 tokens x 151,936 x 5,120 with fp32 output: 447 MB, 69 us at the copy rate.  Measured
-// 196 us, 2.3 TB/s; no pipe is above 40%, so it is the hand-overs between the roles that bound it
-// (167 us without the scales' loads).  16 tokens of the same 119-130 us (floor 64).
+// 210 us after a rest, at 1,965 MHz (2.1 TB/s), and 218 us in a loop, which meets the power limit at
+// about 1,800 MHz; no pipe is above 40%, so it is the hand-overs between the roles that bound it.
+// 16 tokens of the same, bf16 output, 130 us and 32 tokens 137 (floors 64 and 65); 512 tokens x 7,168
+// x 5,120 85 us and 4,096 tokens 561 us, 536 TFLOP/s: each 64 tokens unpack the weights anew.
 #include <algorithm>
 
 #include "kernels.cuh"

@@ -42,7 +42,9 @@
  *  - The library allocates no device memory.  The caller passes a workspace of at least
  *    etree_workspace_size() bytes (256-byte aligned), zeroed once by etree_workspace_init().
  *    One workspace serves one stream at a time.
- *  - The only global state is a per-process cache of TMA descriptors keyed by pointer and shape.
+ *  - The only global state is a per-process cache of TMA descriptors keyed by pointer and shape, and
+ *    what was set up once per context, keyed by the context's id (a scratch address, shared-memory
+ *    limits).
  */
 #ifndef ETREE_H
 #define ETREE_H
@@ -217,7 +219,8 @@ etree_status etree_verify_attn_diff_paged(
 
 /*
  * Products with 4-bit weights and group scales: projections of a target held in 4 bits, and its
- * vocabulary projection, over the nodes of a step.
+ * vocabulary projection, over the nodes of a step.  Logits made here are the caller's to reduce:
+ * etree_lmhead_accept makes its own from bf16 weights.
  *   out[m][n] = bias[n] + sum_k x[m][k] * (q[n][k] - zeros[n][k / group]) * scales[n][k / group]
  *   x        [M] rows of K bf16, x_stride elements apart (a multiple of 8, at least K)
  *   wq       [N][K / 2]: byte k / 2 of a row holds q[k] in its low and q[k + 1] in its high half
@@ -227,7 +230,8 @@ etree_status etree_verify_attn_diff_paged(
  *   out      [M] rows of N bf16 (out_f32 = 0) or fp32 (1), out_stride elements apart, at least N
  * x, wq, scales and zeros are 16-byte aligned; K is a multiple of 32 up to 2^18, 0 <= M <= 65536.
  * No weight is rounded: products with the integers q - zeros are exact and added in fp32, group by
- * group, times the scale.  Results do not depend on timing.  out may not overlap an input.
+ * group, times the scale (values of x below 2^117 cannot overflow a group's sum, whatever the scale
+ * would make of it).  Results do not depend on timing.  out may not overlap an input.
  * One to three launches; the workspace has etree_w4_workspace_size bytes (0 for invalid arguments).
  */
 size_t etree_w4_workspace_size(int M, int N, int K);
@@ -511,9 +515,10 @@ etree_status etree_plan_tree(const etree_cost_table *table, int32_t B, int32_t L
  * both words.  Detail codes:
  *    0  none
  *    1  bad parent: parent[0] != -1 or parent[i] outside [0, i)
- *    2  bad node count: a request with 0 or more than n_max nodes
- *    3  bad kv_len: negative, above kv_len_max, or past the cache pool
- *    4  capacity: kv_len + accepted + 1 > slot_cap
+ *    2  bad node count: a request with 0 or more than n_max nodes (etree_page_plan: a bad cu_new)
+ *    3  bad kv_len: negative, above kv_len_max, or past the cache pool (etree_page_plan: past max_pages,
+ *       or a bad pages_held)
+ *    4  capacity: kv_len + accepted + 1 > slot_cap (etree_page_plan: too few free pages)
  *    5  not a chain: T > 0 on a node with more than one child (etree_lmhead_accept)
  *    6  bad path: path or accept_len out of range in compaction
  *    7  attention wait: a bounded wait gave up in attention
