@@ -191,7 +191,7 @@ etree_status etree_verify_attn_paged(const etree_batch *batch, const int32_t *bl
  *   lambda   [hq] fp32;  norm_w [128] bf16 (16-byte aligned) or NULL;  norm_eps >= 0
  *   lse      [n_total][hq][2] fp32 log-sum-exp of each map's scaled scores; may be NULL
  * scale must be positive.  Other arguments, limits and errors as etree_verify_attn, with a
- * workspace of etree_attn_diff_workspace_size bytes (0 for invalid arguments; at most 85 MB), which also
+ * workspace of etree_attn_diff_workspace_size bytes (0 for invalid arguments; at most 79 MB), which also
  * serves every batch of these heads with no more requests, n_total, n_max and kv_len_max.  Maxima, sums and
  * both maps' outputs are held in fp32; probabilities enter their product with v as two bf16 parts, off
  * by less than 2^-14 of each.
