@@ -400,3 +400,32 @@ def test_one_workspace_as_requests_finish():
         ws = c.ws if ws is None else ws
         c.ws = ws
         c.run(range(min(B, 3)))
+
+
+@pytest.mark.parametrize("kv", [[40, 90], [5000, 4000]])
+@pytest.mark.parametrize("fused", [False, True])
+def test_rows_behind_the_last_request_are_left_as_they_were(kv, fused):
+    """A batch padded to more nodes than its requests have, its spare rows not finite, in one launch and with
+    split keys."""
+    c = Case([3, 4], kv, 4, 2, fused=fused, seed=50)
+    c.run()
+    out, lse = c.out.clone(), c.lse.clone()
+    pad = 1                                  # n_total is at most B * n_max
+    wide = []
+    for t in (c.q, c.kt, c.vt):
+        w = torch.full((c.nt + pad, t.shape[1] * 128 + 8 * fused), float("nan"), dtype=t.dtype, device="cuda")
+        w = w[:, :t.shape[1] * 128].unflatten(1, (t.shape[1], 128))
+        w[:c.nt] = t
+        wide.append(w)
+    c.q, c.kt, c.vt = wide
+    i32 = dict(dtype=torch.int32, device="cuda")
+    parent = torch.cat([c.dev["parent"], torch.full((pad,), -9, **i32)])
+    c.batch = et.make_batch(c.dev["cu"], parent, torch.zeros(c.nt + pad, **i32), c.dev["kv"], c.dev["base"],
+                            torch.zeros(2, **i32), 4, max(kv))
+    c.out = torch.full((c.nt + pad, 4, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    c.lse = torch.full((c.nt + pad, 4, 2), 7.0, device="cuda")
+    c.ws = torch.zeros(et.etree_attn_diff_workspace_size(c.batch, 4, 2), dtype=torch.uint8, device="cuda")
+    c.call()
+    assert et.etree_device_status(c.ws) == (0, 0)
+    assert torch.equal(c.out[:c.nt], out) and torch.equal(c.lse[:c.nt], lse)
+    assert (c.out[c.nt:] == 7.0).all() and (c.lse[c.nt:] == 7.0).all()
